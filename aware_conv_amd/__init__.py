@@ -6,12 +6,19 @@ The layer runs in hand-written HIP kernels behind the C ABI of
 with ctypes.  :class:`WTConv2d` is a drop-in replacement for a depthwise
 ``nn.Conv2d`` that saves only its input for the backward.
 
+Beside the layer: a gated linear recurrence over whole planes or token
+sequences (``include/gscan.h``, :mod:`aware_conv_amd.gscan`,
+:class:`GatedScan2d`) and the AdamW step over many tensors
+(``include/adamw.h``, :mod:`aware_conv_amd.adamw`, :class:`AdamW`).
+
 Nothing is imported eagerly, so ``import aware_conv_amd.build`` works before
 the library exists.
 """
 
 __all__ = ["WTConv2d", "WTConvFunction", "wtconv_fwd", "wtconv_bwd_input",
-           "wtconv_bwd_weight", "wtconv_workspace_size"]
+           "wtconv_bwd_weight", "wtconv_workspace_size",
+           "gscan_fwd", "gscan_bwd", "gscan_step", "gated_scan", "GatedScan2d",
+           "adamw_grad_norm", "adamw_step", "AdamW"]
 
 
 def __getattr__(name):
@@ -22,4 +29,13 @@ def __getattr__(name):
     if name in ("WTConv2d", "WTConvFunction"):
         from . import module
         return getattr(module, name)
+    if name in ("gscan_fwd", "gscan_bwd", "gscan_step", "gated_scan", "GatedScanFunction"):
+        from . import gscan
+        return getattr(gscan, name)
+    if name == "GatedScan2d":
+        from . import module
+        return module.GatedScan2d
+    if name in ("adamw_grad_norm", "adamw_step", "AdamW"):
+        from . import adamw
+        return getattr(adamw, name)
     raise AttributeError(name)

@@ -62,9 +62,48 @@ lib.dwconv_bwd.restype = ctypes.c_int
 lib.wtconv_strerror.argtypes = [ctypes.c_int]
 lib.wtconv_strerror.restype = ctypes.c_char_p
 
+# gscan.h and adamw.h: bound in gscan.py and adamw.py
+class GscanShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("C", ctypes.c_int), ("T", ctypes.c_int),
+                ("layout", ctypes.c_int), ("dtype", ctypes.c_int), ("reverse", ctypes.c_int),
+                ("decay", ctypes.c_float)]
+
+
+class GscanView(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("sr", ctypes.c_longlong)]
+
+
+class AdamwConfig(ctypes.Structure):
+    _fields_ = ([("dtype", ctypes.c_int), ("bits", ctypes.c_int)] +
+                [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay",
+                                                "grad_scale", "max_norm")] +
+                [(n, ctypes.c_void_p) for n in ("lr_dev", "grad_scale_dev", "norm")])
+
+
+_gp, _gv = ctypes.POINTER(GscanShape), ctypes.POINTER(GscanView)
+_szp = ctypes.POINTER(ctypes.c_size_t)
+lib.gscan_states_size.argtypes = [_gp, _szp]
+lib.gscan_workspace_size.argtypes = [_gp, _szp]
+lib.gscan_fwd.argtypes = [_gp] + [_gv] * 3 + [_vp] * 3 + [_gv] + [_vp] * 3 + [ctypes.c_size_t, _vp]
+lib.gscan_bwd.argtypes = ([_gp] + [_gv] * 3 + [_vp] * 3 + [_gv, _vp] + [_gv] * 3 + [_vp] * 3 +
+                          [ctypes.c_size_t, _vp])
+lib.gscan_step.argtypes = ([ctypes.c_int] * 4 + [ctypes.c_float] + [_gv] * 3 + [_vp] * 3 +
+                           [_gv, _vp])
+# tensor lists: host arrays of adamw_tensor
+lib.adamw_workspace_size.argtypes = [_vp, ctypes.c_int, _szp]
+lib.adamw_grad_norm.argtypes = ([ctypes.c_int, _vp, ctypes.c_int, ctypes.c_double] + [_vp] * 3 +
+                                [ctypes.c_size_t, _vp])
+lib.adamw_step.argtypes = ([ctypes.POINTER(AdamwConfig), _vp, ctypes.c_int] + [_vp] * 2 +
+                           [ctypes.c_size_t, _vp])
+for _n in ("gscan_states_size", "gscan_workspace_size", "gscan_fwd", "gscan_bwd", "gscan_step",
+           "adamw_workspace_size", "adamw_grad_norm", "adamw_step"):
+    getattr(lib, _n).restype = ctypes.c_int
+
 EXPORTED = ("wtconv_workspace_size", "wtconv_fwd", "wtconv_bwd_input",
             "wtconv_bwd_weight", "wtconv_bwd", "wtconv_bwd_noalloc", "wtconv_strerror",
-            "dwconv_workspace_size", "dwconv_fwd", "dwconv_bwd")
+            "dwconv_workspace_size", "dwconv_fwd", "dwconv_bwd",
+            "gscan_states_size", "gscan_workspace_size", "gscan_fwd", "gscan_bwd", "gscan_step",
+            "adamw_workspace_size", "adamw_grad_norm", "adamw_step")
 
 
 class WTConvError(RuntimeError):

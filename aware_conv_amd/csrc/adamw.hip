@@ -1,0 +1,442 @@
+// AdamW step over many tensors at once (include/adamw.h) and the global
+// gradient norm.
+//
+// A launch takes a table of tensors by value in its kernel arguments (so
+// nothing is copied or kept, and a captured launch keeps its own); a workgroup
+// takes one chunk of one tensor.  The step is bound by HBM: it reads and
+// writes each value once, 16 bytes per lane and access where the type allows.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "adamw_internal.h"
+#include "gscan_math.h"
+
+namespace adw {
+namespace {
+
+using gsc::BF16;
+using gsc::F16;
+using gsc::F32;
+using gsc::Raw;
+
+constexpr int kThreads = 256;
+constexpr int kVec = 4;                           // elements of a lane and access
+constexpr int kUnits = 4;                         // accesses of a lane
+constexpr int kChunk = kThreads * kVec * kUnits;  // elements of a workgroup
+
+// P pointers for each of up to N tensors, and the chunks before each.
+template <int P, int N>
+struct Table {
+    void* ptr[P][N];
+    long long n[N];
+    int first[N + 1];
+    int count;
+};
+// as many tensors as 4 KiB of kernel arguments hold, less 96 bytes for the rest
+template <int P>
+constexpr int kFit = (4096 - 96) / (8 * P + 8 + 4);
+
+// The tensor that holds chunk `blk`.
+template <int P, int N>
+__device__ __forceinline__ int tensor_of(const Table<P, N>& t, int blk) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (t.first[mid] <= blk) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <class D>
+__device__ __forceinline__ Raw<D, kVec> fetch(const typename D::S* p, int n) {
+    Raw<D, kVec> q;
+    if (n >= kVec) {
+        gsc::load_vec<D, kVec>(q, p);
+    } else {
+#pragma unroll
+        for (int k = 0; k < Raw<D, kVec>::kWords; ++k) q.w[k] = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) q.set(j, gsc::load_one<D>(p + j));
+    }
+    return q;
+}
+template <class D>
+__device__ __forceinline__ void put(typename D::S* p, const float (&v)[kVec], int n) {
+    if (n >= kVec) {
+        Raw<D, kVec> q;
+#pragma unroll
+        for (int k = 0; k < Raw<D, kVec>::kWords; ++k) q.w[k] = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) q.set(j, v[j]);
+        gsc::store_vec<D, kVec>(p, q);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) gsc::store_one<D>(p + j, v[j]);
+    }
+}
+
+// Four codes in a word.
+__device__ __forceinline__ uint32_t fetch_codes(const uint8_t* p, int n) {
+    uint32_t w = 0;
+    if (n >= kVec) {
+        struct __attribute__((packed, aligned(1))) P { uint32_t w; };
+        w = reinterpret_cast<const P*>(p)->w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) w |= uint32_t(p[j]) << (8 * j);
+    }
+    return w;
+}
+__device__ __forceinline__ void put_codes(uint8_t* p, uint32_t w, int n) {
+    if (n >= kVec) {
+        struct __attribute__((packed, aligned(1))) P { uint32_t w; };
+        reinterpret_cast<P*>(p)->w = w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) p[j] = uint8_t(w >> (8 * j));
+    }
+}
+__device__ __forceinline__ void decode(uint32_t w, float (&v)[kVec]) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
+    v[0] = lo[0];
+    v[1] = lo[1];
+    v[2] = hi[0];
+    v[3] = hi[1];
+}
+
+// Largest of the wavefront's non-negative values, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// The magnitude's code (as the value it stands for) for x >= 0 in units of the
+// scale and dither d.  Codes are 8 steps per power of two down to 2^-6, and
+// evenly spaced below.  x / ulp is exact (ulp is a power of two), below 16, so
+// adding d loses at most 2^-21 of a step.
+__device__ __forceinline__ float code_of(float x, float d) {
+    const uint32_t e = max(__float_as_uint(x) & 0x7f800000u, 0x3c800000u);  // 2^exponent, at least 2^-6
+    const float ulp = __uint_as_float(e - (3u << 23));
+    const float per = __uint_as_float((254u << 23) - (e - (3u << 23)));  // 1 / ulp
+    const float q = fminf(floorf(fmaf(x, per, d)) * ulp, 448.f);
+    return x <= 3e38f ? q : __uint_as_float(0x7fc00000u);
+}
+
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a <= 3e38f ? a : 0.f;
+}
+
+// Codes and scale of a block of the wavefront (four elements per lane).
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode(const float (&v)[kVec], uint32_t k, uint32_t turn,
+                                           float& scale) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) top = fmaxf(top, finite_abs(v[j]));
+    scale = wave_max(top) * (1.f / 448.f);
+    const bool live = scale >= 1.17549435e-38f;
+    scale = live ? scale : 0.f;
+    const float inv = live ? 1.f / scale : 0.f;
+    float c[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        const uint32_t u = (k + j) * 2654435769u + turn + (ROOT ? 0x80000000u : 0u);
+        const float d = float(u >> 8) * 0x1p-24f;
+        const float x = fabsf(v[j]) * inv;
+        c[j] = code_of(x, d);
+        if (ROOT) c[j] = x > 0.f && c[j] == 0.f ? 0x1p-9f : c[j];
+        else c[j] = copysignf(c[j], v[j]);
+    }
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    return uint32_t(w);
+}
+
+// One thread: the step's number and its coefficients.
+__global__ void k_begin(int* step, const float* lr_dev, const float* scale_dev, const float* norm,
+                        double lr, double beta1, double beta2, double decay, double scale,
+                        double max_norm, Ctl* ctl) {
+    Ctl c;
+    const int t = *step + 1;
+    if (lr_dev) lr = double(*lr_dev);
+    if (scale_dev) scale = double(*scale_dev);
+    c.on = 1;
+    if (norm) {
+        const float n = *norm;
+        c.on = fabsf(n) <= 3.4028235e38f;
+        if (max_norm > 0) scale *= fmin(1.0, max_norm / (double(n) + 1e-6));
+    }
+    c.keep = float(1.0 - lr * decay);
+    c.rate = float(lr / (1.0 - pow(beta1, double(t))));
+    c.root = float(1.0 / sqrt(1.0 - pow(beta2, double(t))));
+    c.scale = scale;
+    c.turn = unsigned(t) * 3242174889u;
+    if (c.on) *step = t;
+    *ctl = c;
+}
+
+struct Betas {
+    double b1, o1;  // o = 1 - b
+    float b2, o2, eps;
+};
+
+// New moments and parameter of one element; m0 is factor * scale.  The two
+// terms of m may cancel, which would leave an fp32 sum with few of its digits
+// for a parameter whose v is small: m is formed in fp64, whose few
+// instructions hide behind the memory accesses, and rounded once.
+__device__ __forceinline__ void advance(float& p, float factor, float scale, float& m, float& v,
+                                        float g, const Ctl& c, const Betas& h, float& s) {
+    const double gd = double(g) * c.scale;
+    m = float(fma(h.b1, double(factor) * double(scale), h.o1 * gd));
+    g = float(gd);
+    v = fmaf(h.b2, v, (h.o2 * g) * g);
+    s = gsc::sqrt_hw(v);
+    p = fmaf(p, c.keep, -c.rate * m * gsc::rcp_hw(fmaf(s, c.root, h.eps)));
+}
+
+enum { P_, G_, M_, V_, X0_ };  // then: master, and/or the two scales
+
+template <class D, bool BITS8, bool MASTER>
+constexpr int kPtrs = 4 + (MASTER ? 1 : 0) + (BITS8 ? 2 : 0);
+
+template <class D, bool BITS8, bool MASTER>
+__global__ __launch_bounds__(kThreads) void k_step(
+    Table<kPtrs<D, BITS8, MASTER>, kFit<kPtrs<D, BITS8, MASTER>>> t, const Ctl* ctl, Betas h) {
+    using S = typename D::S;
+    const Ctl c = *ctl;
+    if (!c.on) return;
+    const int id = tensor_of(t, blockIdx.x);
+    const long long n = t.n[id];
+    const long long base = (long long)(int(blockIdx.x) - t.first[id]) * kChunk;
+    S* p = static_cast<S*>(t.ptr[P_][id]);
+    const S* g = static_cast<const S*>(t.ptr[G_][id]);
+    float* w = MASTER ? static_cast<float*>(t.ptr[X0_][id]) : nullptr;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const long long k = base + (u * kThreads + threadIdx.x) * kVec;
+        const int left = int(n - k < kVec ? (n - k > 0 ? n - k : 0) : kVec);
+        const Raw<D, kVec> qg = fetch<D>(g + k, left);
+        float pv[kVec], mv[kVec], vv[kVec], sv[kVec];
+        if constexpr (MASTER) {
+            const Raw<F32, kVec> qw = fetch<F32>(w + k, left);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) pv[j] = qw.get(j);
+        } else {
+            const Raw<D, kVec> qp = fetch<D>(p + k, left);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) pv[j] = qp.get(j);
+        }
+        if constexpr (BITS8) {
+            uint8_t* m = static_cast<uint8_t*>(t.ptr[M_][id]);
+            uint8_t* v = static_cast<uint8_t*>(t.ptr[V_][id]);
+            float* ms = static_cast<float*>(t.ptr[X0_ + MASTER][id]);
+            float* vs = static_cast<float*>(t.ptr[X0_ + MASTER + 1][id]);
+            // a wavefront's 256 elements are one block
+            const long long blk = (base + (u * kThreads + threadIdx.x / 64 * 64) * kVec) / ADAMW_BLOCK;
+            const bool any = blk * ADAMW_BLOCK < n;
+            const float sm = any ? ms[blk] : 0.f, sr = any ? vs[blk] : 0.f;
+            decode(fetch_codes(m + k, left), mv);
+            decode(fetch_codes(v + k, left), vv);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                vv[j] *= sr;
+                vv[j] *= vv[j];
+                advance(pv[j], mv[j], sm, mv[j], vv[j], qg.get(j), c, h, sv[j]);
+            }
+            float a, b;
+            const uint32_t cm = encode<false>(mv, uint32_t(k), c.turn, a);
+            const uint32_t cv = encode<true>(sv, uint32_t(k), c.turn, b);
+            put_codes(m + k, cm, left);
+            put_codes(v + k, cv, left);
+            if (any && threadIdx.x % 64 == 0) {
+                ms[blk] = a;
+                vs[blk] = b;
+            }
+        } else {
+            float* m = static_cast<float*>(t.ptr[M_][id]);
+            float* v = static_cast<float*>(t.ptr[V_][id]);
+            const Raw<F32, kVec> qm = fetch<F32>(m + k, left), qv = fetch<F32>(v + k, left);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                mv[j] = qm.get(j);
+                vv[j] = qv.get(j);
+                advance(pv[j], mv[j], 1.f, mv[j], vv[j], qg.get(j), c, h, sv[j]);
+            }
+            put<F32>(m + k, mv, left);
+            put<F32>(v + k, vv, left);
+        }
+        if constexpr (MASTER) put<F32>(w + k, pv, left);
+        put<D>(p + k, pv, left);
+    }
+}
+
+template <class D>
+__global__ __launch_bounds__(kThreads) void k_squares(Table<1, kFit<1>> t, double* part) {
+    using S = typename D::S;
+    __shared__ double acc[kThreads / 64];
+    const int id = tensor_of(t, blockIdx.x);
+    const long long n = t.n[id];
+    const long long base = (long long)(int(blockIdx.x) - t.first[id]) * kNormChunk;
+    const S* g = static_cast<const S*>(t.ptr[0][id]);
+    // fp64 from the first product: the sum of squares of fp32 values may leave
+    // fp32's range, and the conversion costs less than the memory access
+    double s = 0;
+#pragma unroll 4
+    for (int u = 0; u < int(kNormChunk) / (kThreads * kVec); ++u) {
+        const long long k = base + (u * kThreads + threadIdx.x) * kVec;
+        const int left = int(n - k < kVec ? (n - k > 0 ? n - k : 0) : kVec);
+        const Raw<D, kVec> q = fetch<D>(g + k, left);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const double v = double(q.get(j));
+            s = fma(v, v, s);
+        }
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
+    if (threadIdx.x % 64 == 0) acc[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < kThreads / 64; ++k) s += acc[k];
+        part[blockIdx.x] = s;
+    }
+}
+
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void k_norm(const double* part, long long parts,
+                                                      double scale, const float* scale_dev,
+                                                      float* norm) {
+    __shared__ double acc[kSumThreads / 64];
+    double s = 0;
+    for (long long k = threadIdx.x; k < parts; k += kSumThreads) s += part[k];
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
+    if (threadIdx.x % 64 == 0) acc[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < kSumThreads / 64; ++k) s += acc[k];
+        if (scale_dev) scale = double(*scale_dev);
+        *norm = float(fabs(scale) * sqrt(s));
+    }
+}
+
+// Chunks of one launch (threads of a grid are below 2^32); no tensor has more.
+constexpr long long kMaxChunks = 1LL << 23;
+
+// Calls launch(table, chunks) for the tensors of a list, as many to a launch
+// as a table and a grid hold.
+template <int P, int N, class Ptrs, class Launch>
+hipError_t in_tables(const adamw_tensor* list, int count, long long chunk, Ptrs ptrs, Launch launch) {
+    Table<P, N> t;
+    t.count = 0;
+    t.first[0] = 0;
+    auto flush = [&]() -> hipError_t {
+        if (t.count == 0) return hipSuccess;
+        launch(t, t.first[t.count]);
+        t.count = 0;
+        return hipGetLastError();
+    };
+    for (int i = 0; i < count; ++i) {
+        if (list[i].n == 0) continue;
+        const long long chunks = (list[i].n + chunk - 1) / chunk;
+        if (t.count == N || t.first[t.count] + chunks > kMaxChunks) {
+            const hipError_t e = flush();
+            if (e != hipSuccess) return e;
+        }
+        void* p[P];
+        ptrs(list[i], p);
+        for (int k = 0; k < P; ++k) t.ptr[k][t.count] = p[k];
+        t.n[t.count] = list[i].n;
+        t.first[t.count + 1] = t.first[t.count] + int(chunks);
+        ++t.count;
+    }
+    return flush();
+}
+
+template <class D, bool BITS8, bool MASTER>
+hipError_t run_step(const adamw_tensor* list, int count, const Ctl* ctl, const Betas& h,
+                    hipStream_t st) {
+    constexpr int P = kPtrs<D, BITS8, MASTER>;
+    return in_tables<P, kFit<P>>(
+        list, count, kChunk,
+        [](const adamw_tensor& t, void** p) {
+            p[P_] = t.p;
+            p[G_] = const_cast<void*>(t.g);
+            p[M_] = t.m;
+            p[V_] = t.v;
+            if (MASTER) p[X0_] = t.w;
+            if (BITS8) {
+                p[X0_ + MASTER] = t.ms;
+                p[X0_ + MASTER + 1] = t.vs;
+            }
+        },
+        [&](const Table<P, kFit<P>>& t, int chunks) {
+            k_step<D, BITS8, MASTER><<<dim3(chunks), kThreads, 0, st>>>(t, ctl, h);
+        });
+}
+template <class D>
+hipError_t run_type(bool bits8, bool master, const adamw_tensor* list, int count, const Ctl* ctl,
+                    const Betas& h, hipStream_t st) {
+    if (bits8)
+        return master ? run_step<D, true, true>(list, count, ctl, h, st)
+                      : run_step<D, true, false>(list, count, ctl, h, st);
+    return master ? run_step<D, false, true>(list, count, ctl, h, st)
+                  : run_step<D, false, false>(list, count, ctl, h, st);
+}
+
+template <class D>
+hipError_t run_squares(const adamw_tensor* list, int count, double* part, long long* parts,
+                       hipStream_t st) {
+    long long before = 0;
+    const hipError_t e = in_tables<1, kFit<1>>(
+        list, count, kNormChunk,
+        [](const adamw_tensor& t, void** p) { p[0] = const_cast<void*>(t.g); },
+        [&](const Table<1, kFit<1>>& t, int chunks) {
+            k_squares<D><<<dim3(chunks), kThreads, 0, st>>>(t, part + before);
+            before += chunks;
+        });
+    *parts = before;
+    return e;
+}
+
+}  // namespace
+
+hipError_t grad_norm(int dtype, const adamw_tensor* t, int count, double scale,
+                     const float* scale_dev, float* norm, double* part, hipStream_t st) {
+    long long parts = 0;
+    hipError_t e;
+    if (dtype == ADAMW_F32) e = run_squares<F32>(t, count, part, &parts, st);
+    else if (dtype == ADAMW_F16) e = run_squares<F16>(t, count, part, &parts, st);
+    else e = run_squares<BF16>(t, count, part, &parts, st);
+    if (e != hipSuccess) return e;
+    k_norm<<<1, kSumThreads, 0, st>>>(part, parts, scale, scale_dev, norm);
+    return hipGetLastError();
+}
+
+hipError_t step(const adamw_config& c, const adamw_tensor* t, int count, int* step, Ctl* ctl,
+                hipStream_t st) {
+    k_begin<<<1, 1, 0, st>>>(step, c.lr_dev, c.grad_scale_dev, c.norm, c.lr, c.beta1, c.beta2,
+                             c.weight_decay, c.grad_scale, c.max_norm, ctl);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const Betas h{c.beta1, 1.0 - c.beta1, float(c.beta2), float(1.0 - c.beta2),
+                  float(c.eps)};
+    bool master = false;
+    for (int i = 0; i < count && !master; ++i) master = t[i].n > 0 && t[i].w;
+    if (c.dtype == ADAMW_F32) return run_type<F32>(c.bits == 8, master, t, count, ctl, h, st);
+    if (c.dtype == ADAMW_F16) return run_type<F16>(c.bits == 8, master, t, count, ctl, h, st);
+    return run_type<BF16>(c.bits == 8, master, t, count, ctl, h, st);
+}
+
+}  // namespace adw

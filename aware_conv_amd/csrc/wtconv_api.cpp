@@ -462,6 +462,8 @@ const char* wtconv_strerror(int code) {
         case WTCONV_ERR_ALIAS: return "an output overlaps an input or another output";
         case WTCONV_ERR_SCRATCH:
             return "shape needs more workspace than wtconv_bwd_noalloc's static scratch holds";
+        case WTCONV_ERR_LAYOUT: return "unknown layout, negative stride or overlapping rows";
+        case WTCONV_ERR_VALUE: return "a coefficient is outside its range";
         case WTCONV_ERR_HIP: return "a HIP kernel launch failed";
         default: return "unknown error code";
     }

@@ -1,7 +1,9 @@
 """torch.autograd and nn.Module wrappers over the C ABI."""
+import math
+
 import torch
 
-from . import _lib
+from . import _lib, gscan
 
 
 class WTConvFunction(torch.autograd.Function):
@@ -52,3 +54,34 @@ class WTConv2d(torch.nn.Module):
     def forward(self, x):
         return WTConvFunction.apply(x.contiguous(), self.w_base, self.b_base, self.s_base,
                                     self.w_wav, self.s_wav)
+
+
+class GatedScan2d(torch.nn.Module):
+    """Gated linear recurrence over whole planes [B, C, H, W] in raster order, its gates two
+    WTConv layers of the input: each output mixes all positions before it (and, where ``both``,
+    in a second recurrence from the end, all positions after it).
+
+    lam is fp32 whatever the layer's dtype; at a fully open gate the decays start evenly spread
+    over ``decay_range``."""
+
+    DECAY = 8.0
+
+    def __init__(self, channels, kernel_size=5, levels=2, both=True, decay_range=(0.9, 0.999),
+                 device=None, dtype=None):
+        super().__init__()
+        f = {"device": device, "dtype": dtype}
+        self.reset = WTConv2d(channels, kernel_size, levels, **f)
+        self.input = WTConv2d(channels, kernel_size, levels, **f)
+        lo, hi = decay_range
+        a = torch.linspace(lo, hi, channels, dtype=torch.float64)
+        lam = torch.log(torch.expm1(-torch.log(a) / self.DECAY)).float()
+        self.lam = torch.nn.Parameter(lam.repeat(2 if both else 1, 1).to(device))
+        self.scale = 1 / math.sqrt(2) if both else 1.0
+
+    def forward(self, x):
+        x = x.contiguous()
+        r, i = self.reset(x), self.input(x)
+        h = gscan.gated_scan(x, r, i, self.lam[0], decay=self.DECAY)[0]
+        if len(self.lam) == 2:
+            h = h + gscan.gated_scan(x, r, i, self.lam[1], reverse=True, decay=self.DECAY)[0]
+        return h * self.scale

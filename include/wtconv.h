@@ -98,6 +98,9 @@ typedef struct {
                                        the workspace overlaps any buffer of the call */
 #define WTCONV_ERR_SCRATCH (-10)    /* wtconv_bwd_noalloc: the shape needs more workspace
                                        than WTCONV_NOALLOC_SCRATCH_BYTES */
+#define WTCONV_ERR_LAYOUT (-11)     /* gscan.h: unknown layout, a negative stride, or an output
+                                       whose rows overlap */
+#define WTCONV_ERR_VALUE (-12)      /* gscan.h, adamw.h: a coefficient outside its range */
 #define WTCONV_ERR_HIP (-100)       /* a kernel launch failed */
 
 /*
