@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "gscan.h"
+#include "gscan_carry.h"
 
 namespace gsc {
 
@@ -22,6 +23,7 @@ struct Args {
     const int* lengths;
     float *h_last, *states, *dlam, *dh0;
     float* part;  // partial sums of dlam, [parts][C]
+    Carry carry;  // where tiles are spread over workgroups
     int B, C, T, tiles;
     float decay;
 };

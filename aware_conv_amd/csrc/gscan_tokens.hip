@@ -1,12 +1,13 @@
 // Gated linear recurrence over tokens ([B][T][C], channels contiguous), and
 // its form for one position.
 //
-// A workgroup takes 64 channels of one sequence and walks tiles of kSub * kLen
-// positions.  A thread takes two neighbouring channels and kLen consecutive
+// A workgroup takes a tile of kSub * kLen positions of 64 channels of one
+// sequence.  A thread takes two neighbouring channels and kLen consecutive
 // positions: it composes their maps h -> a h + b in registers, the kSub
 // compositions of a channel meet in LDS, and each thread runs its positions
-// again from the state that it then knows.  Everything is read once and
-// written once.
+// again from the state that it then knows.  The state passes from tile to tile
+// between workgroups (gscan_carry.h).  Everything is read once and written
+// once.
 #include <hip/hip_runtime.h>
 
 #include "gscan_math.h"
@@ -45,32 +46,56 @@ __device__ __forceinline__ void put2(typename D::S* p, float v0, float v1, int n
     }
 }
 
-// What a thread works on.
+// What a thread works on.  `SPREAD`: the tiles of a sequence are spread over
+// workgroups (gscan_carry.h), units in the order of the tiles.
 struct Me {
-    int b, c, n;  // sequence, first channel, channels that exist
-    int cl, sub;  // place in the tile
-    int len;
+    int b, c, n;   // sequence, first channel, channels that exist
+    int cl, sub;   // place in the tile
+    int len;       // valid positions of the sequence
+    int valid;     // its tiles that hold any
+    int m;         // place of the tile in the order of the scan
 };
-__device__ __forceinline__ Me me_of(const Args& g) {
-    Me m;
+__device__ __forceinline__ Me me_of(const Args& g, unsigned unit) {
+    Me me;
     const unsigned wide = (g.C + kChan - 1) / kChan;
-    m.b = blockIdx.x / wide;
-    m.cl = threadIdx.x % kLanes;
-    m.sub = threadIdx.x / kLanes;
-    m.c = (blockIdx.x % wide) * kChan + 2 * m.cl;
-    m.n = min(max(g.C - m.c, 0), 2);
-    m.len = g.T;
-    if (g.lengths) m.len = min(max(g.lengths[m.b], 0), g.T);
-    return m;
+    const unsigned side = unit / wide;
+    me.m = side / unsigned(g.B);
+    me.b = side - me.m * unsigned(g.B);
+    me.cl = threadIdx.x % kLanes;
+    me.sub = threadIdx.x / kLanes;
+    me.c = (unit - side * wide) * kChan + 2 * me.cl;
+    me.n = min(max(g.C - me.c, 0), 2);
+    me.len = g.T;
+    if (g.lengths) me.len = min(max(g.lengths[me.b], 0), g.T);
+    me.valid = (me.len + kTile - 1) / kTile;
+    return me;
 }
 
-// First element of the thread's channels at scan position p (< len), or at
-// its own index beyond.
+// The thread's channels at its positions: `p` points at the first, `step`
+// (the same for all threads) leads from one to the next.
 template <class S>
-__device__ __forceinline__ S* place(const void* base, long long sb, long long sr, const Me& m,
-                                    int p, bool rev) {
-    const int t = rev && p < m.len ? m.len - 1 - p : p;
-    return const_cast<S*>(static_cast<const S*>(base)) + m.b * sb + t * sr + m.c;
+struct Run {
+    S* p;
+    long long step;
+    __device__ __forceinline__ S* at(int j) const { return p + j * step; }
+};
+template <class S>
+__device__ __forceinline__ Run<S> run_of(const void* base, long long sb, long long sr, const Me& m,
+                                         int p0, bool rev) {
+    const int t = rev ? m.len - 1 - p0 : p0;
+    return Run<S>{const_cast<S*>(static_cast<const S*>(base)) + m.b * sb + t * sr + m.c,
+                  rev ? -sr : sr};
+}
+
+// A thread's positions.  FULL: all of the tile are valid, all its channels exist.
+template <class D, bool FULL>
+__device__ __forceinline__ void fetch_run(Raw<D, 2> (&q)[kLen], const Run<const typename D::S>& r,
+                                          const Me& m, int p0) {
+#pragma unroll
+    for (int j = 0; j < kLen; ++j) q[j] = fetch2<D>(r.at(j), FULL ? 2 : p0 + j < m.len ? m.n : 0);
+}
+__device__ __forceinline__ bool full_tile(const Args& g, const Me& m, int tile) {
+    return m.c - 2 * m.cl + kChan <= g.C && (tile + 1) * kTile <= m.len;
 }
 
 struct Two {
@@ -82,193 +107,327 @@ __device__ __forceinline__ void rates(const Args& g, const Me& m, float (&rate)[
     rate[1] = m.n > 1 ? g.decay * softplus(g.lam[m.c + 1]) * kLog2e : 0.f;
 }
 
+__device__ __forceinline__ float2 load_row(const float* p, const Me& m) {
+    float2 s{0.f, 0.f};
+    if (p && m.n > 0) s.x = p[0];
+    if (p && m.n > 1) s.y = p[1];
+    return s;
+}
+__device__ __forceinline__ void store_row(float* p, const Me& m, float2 s) {
+    if (m.n > 0) p[0] = s.x;
+    if (m.n > 1) p[1] = s.y;
+}
+
+// Zeros at the padding among the thread's positions from p0 on (at its own
+// index in both directions).
 template <class D>
-__global__ __launch_bounds__(kThreads) void k_tokens_fwd(Args g, bool rev) {
+__device__ __forceinline__ void pad(const Args& g, void* out, long long sb, long long sr,
+                                    const Me& m, int p0) {
     using S = typename D::S;
-    __shared__ Two part[2][kSub][kLanes];
-    __shared__ float2 state[2][kLanes];
-    const Me m = me_of(g);
-    const size_t at = size_t(m.b) * g.C + m.c;
-    float rate[2];
-    rates(g, m, rate);
-    if (m.sub == 0) {
-        float2 s{0.f, 0.f};
-        if (g.h0 && m.n > 0) s.x = g.h0[at];
-        if (g.h0 && m.n > 1) s.y = g.h0[at + 1];
-        state[0][m.cl] = s;
-    }
-    for (int n = 0; n < g.tiles; ++n) {
-        const int p0 = n * kTile + m.sub * kLen;
-        Raw<D, 2> qx[kLen], qr[kLen], qi[kLen];
-#pragma unroll
-        for (int j = 0; j < kLen; ++j) {
-            const int k = p0 + j < m.len ? m.n : 0;
-            qx[j] = fetch2<D>(place<const S>(g.x, g.x_sb, g.x_sr, m, p0 + j, rev), k);
-            qr[j] = fetch2<D>(place<const S>(g.r, g.r_sb, g.r_sr, m, p0 + j, rev), k);
-            qi[j] = fetch2<D>(place<const S>(g.i, g.i_sb, g.i_sr, m, p0 + j, rev), k);
+    const Run<S> q = run_of<S>(out, sb, sr, m, p0, false);
+    for (int j = max(m.len - p0, 0); j < kLen; ++j)
+        if (p0 + j < g.T) put2<D>(q.at(j), 0.f, 0.f, m.n);
+}
+
+// What a tile needs of the tiles before it: each row of threads along time
+// waits for one word, so that all are on their way together and few registers
+// hold them.  Row k takes the map of the k-th tile of the group, the last row
+// the state at the group's start.
+__device__ __forceinline__ Two await(const Args& g, const Me& m) {
+    const int grp = m.m / kGroup, k = m.m % kGroup;
+    Two t{1.f, 0.f, 1.f, 0.f};
+    if (m.n == 0) return t;
+    if (m.sub < k) {
+        const unsigned long long* p =
+            g.carry.maps + (size_t(grp * kGroup + m.sub) * g.B + m.b) * g.C + m.c;
+        unsigned long long w0, w1;
+        for (;;) {
+            w0 = peek_map(p);
+            w1 = m.n > 1 ? peek_map(p + 1) : 0;
+            if (w0 != ~0ull && w1 != ~0ull) break;
+            __builtin_amdgcn_s_sleep(1);
         }
-        float a[2][kLen], b[2][kLen], A[2], H[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            A[e] = 1.f;
-            H[e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < kLen; ++j) {
-                gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], b[e][j]);
-                if (p0 + j >= m.len) {
-                    a[e][j] = 1.f;
-                    b[e][j] = 0.f;
-                }
-                H[e] = fmaf(a[e][j], H[e], b[e][j]);
-                A[e] *= a[e][j];
+        t = Two{map_a(w0), map_h(w0), map_a(w1), map_h(w1)};
+    } else if (m.sub == kSub - 1 && grp > 0) {
+        const unsigned* p = g.carry.starts + (size_t(grp) * g.B + m.b) * g.C + m.c;
+        unsigned w0, w1;
+        for (;;) {
+            w0 = peek_start(p);
+            w1 = m.n > 1 ? peek_start(p + 1) : 0;
+            if (w0 != ~0u && w1 != ~0u) break;
+            __builtin_amdgcn_s_sleep(1);
+        }
+        t.h0 = __uint_as_float(w0);
+        t.h1 = __uint_as_float(w1);
+    }
+    return t;
+}
+
+// Shared by both directions: the state before the tile for the thread's
+// channels, from `first`, that before the whole scan.  Call after the threads'
+// maps were stored; their composition, `map_of`, is published by row `last`.
+template <bool SPREAD, class Map>
+__device__ __forceinline__ float2 before_tile(const Args& g, const Me& m, const float* first,
+                                              Two (*look)[kLanes], int last, Map map_of) {
+    static_assert(kGroup - 1 < kSub, "a row of threads for each word");
+    const size_t at = size_t(m.b) * g.C + m.c;
+    __syncthreads();
+    if (SPREAD && m.sub == last && m.m + 1 < m.valid && m.m % kGroup != kGroup - 1) {
+        const Two t = map_of();
+        unsigned long long* p = g.carry.maps + (size_t(m.m) * g.B + m.b) * g.C + m.c;
+        if (m.n > 0) publish_map(p, t.a0, t.h0);
+        if (m.n > 1) publish_map(p + 1, t.a1, t.h1);
+    }
+    float2 s = load_row(first && (!SPREAD || m.m < kGroup) ? first + at : nullptr, m);
+    if constexpr (SPREAD) {
+        if (m.m > 0) {
+            look[m.sub][m.cl] = await(g, m);
+            __syncthreads();
+            if (m.m >= kGroup) s = float2{look[kSub - 1][m.cl].h0, look[kSub - 1][m.cl].h1};
+            for (int k = 0; k < m.m % kGroup; ++k) {
+                const Two t = look[k][m.cl];
+                s.x = fmaf(t.a0, s.x, t.h0);
+                s.y = fmaf(t.a1, s.y, t.h1);
             }
         }
-        // two buffers, by turns: what the next tile writes, nobody still reads
-        part[n & 1][m.sub][m.cl] = Two{A[0], H[0], A[1], H[1]};
-        __syncthreads();
-        float2 s = state[n & 1][m.cl];
-        if (m.sub == 0 && g.states) {
-            float* q = g.states + size_t(n) * g.B * g.C + at;
-            if (m.n > 0) q[0] = s.x;
-            if (m.n > 1) q[1] = s.y;
-        }
-        for (int k = 0; k < m.sub; ++k) {
-            const Two t = part[n & 1][k][m.cl];
-            s.x = fmaf(t.a0, s.x, t.h0);
-            s.y = fmaf(t.a1, s.y, t.h1);
-        }
-#pragma unroll
-        for (int j = 0; j < kLen; ++j) {
-            s.x = fmaf(a[0][j], s.x, b[0][j]);
-            s.y = fmaf(a[1][j], s.y, b[1][j]);
-            const bool in = p0 + j < m.len;
-            put2<D>(place<S>(g.h, g.h_sb, g.h_sr, m, p0 + j, rev), in ? s.x : 0.f, in ? s.y : 0.f,
-                    p0 + j < g.T ? m.n : 0);
-        }
-        if (m.sub == kSub - 1) state[(n + 1) & 1][m.cl] = s;
     }
-    if (m.sub == kSub - 1 && g.h_last) {
-        const float2 s = state[g.tiles & 1][m.cl];  // this thread's own store
-        if (m.n > 0) g.h_last[at] = s.x;
-        if (m.n > 1) g.h_last[at + 1] = s.y;
+    return s;
+}
+
+// After the last position of the scan's order in this tile, at state s.
+template <bool SPREAD>
+__device__ __forceinline__ void after_tile(const Args& g, const Me& m, float* last, float2 s) {
+    if (SPREAD && m.m + 1 < m.valid) {
+        if (m.m % kGroup == kGroup - 1) {
+            unsigned* p = g.carry.starts + (size_t(m.m / kGroup + 1) * g.B + m.b) * g.C + m.c;
+            if (m.n > 0) publish_start(p, s.x);
+            if (m.n > 1) publish_start(p + 1, s.y);
+        }
+    } else if (last) {
+        store_row(last + size_t(m.b) * g.C + m.c, m, s);
     }
 }
 
-template <class D>
-__global__ __launch_bounds__(kThreads) void k_tokens_bwd(Args g, bool rev) {
+template <bool SPREAD>
+__device__ __forceinline__ unsigned my_unit(const Args& g, unsigned* shared) {
+    if constexpr (!SPREAD) return blockIdx.x;
+    if (threadIdx.x == 0) *shared = take_unit(g.carry);
+    __syncthreads();
+    return *shared;
+}
+
+struct FwdShared {
+    Two part[kSub][kLanes], look[kSub][kLanes];
+    unsigned unit;
+};
+
+// FULL: all positions of the tile are valid and all its channels exist.
+template <class D, bool SPREAD, bool FULL>
+__device__ __forceinline__ void tile_fwd(const Args& g, const Me& m, bool rev, FwdShared& sh) {
     using S = typename D::S;
-    __shared__ Two part[2][kSub][kLanes];   // maps of h
-    __shared__ float2 upart[2][kSub][kLanes];  // and of u (the factors are the same)
-    __shared__ float2 ustate[2][kLanes];
-    const Me m = me_of(g);
+    auto& part = sh.part;
     const size_t at = size_t(m.b) * g.C + m.c;
+    const int p0 = m.m * kTile + m.sub * kLen;
+    Raw<D, 2> qx[kLen], qr[kLen], qi[kLen];
+    fetch_run<D, FULL>(qx, run_of<const S>(g.x, g.x_sb, g.x_sr, m, p0, rev), m, p0);
+    fetch_run<D, FULL>(qr, run_of<const S>(g.r, g.r_sb, g.r_sr, m, p0, rev), m, p0);
+    fetch_run<D, FULL>(qi, run_of<const S>(g.i, g.i_sb, g.i_sr, m, p0, rev), m, p0);
+    float rate[2];
+    rates(g, m, rate);
+    float a[2][kLen], b[2][kLen], A[2], H[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        A[e] = 1.f;
+        H[e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) {
+            gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], b[e][j]);
+            if (!FULL && p0 + j >= m.len) {
+                a[e][j] = 1.f;
+                b[e][j] = 0.f;
+            }
+            H[e] = fmaf(a[e][j], H[e], b[e][j]);
+            A[e] *= a[e][j];
+        }
+    }
+    part[m.sub][m.cl] = Two{A[0], H[0], A[1], H[1]};
+    float2 s = before_tile<SPREAD>(g, m, g.h0, sh.look, kSub - 1, [&] {
+        Two t = part[0][m.cl];
+#pragma unroll 3
+        for (int k = 1; k < kSub; ++k) {
+            const Two q = part[k][m.cl];
+            t = Two{q.a0 * t.a0, fmaf(q.a0, t.h0, q.h0), q.a1 * t.a1, fmaf(q.a1, t.h1, q.h1)};
+        }
+        return t;
+    });
+    if (m.sub == 0 && g.states) store_row(g.states + size_t(m.m) * g.B * g.C + at, m, s);
+    for (int k = 0; k < m.sub; ++k) {
+        const Two t = part[k][m.cl];
+        s.x = fmaf(t.a0, s.x, t.h0);
+        s.y = fmaf(t.a1, s.y, t.h1);
+    }
+    const Run<S> out = run_of<S>(g.h, g.h_sb, g.h_sr, m, p0, rev);
+#pragma unroll
+    for (int j = 0; j < kLen; ++j) {
+        s.x = fmaf(a[0][j], s.x, b[0][j]);
+        s.y = fmaf(a[1][j], s.y, b[1][j]);
+        if (FULL || p0 + j < m.len) put2<D>(out.at(j), s.x, s.y, FULL ? 2 : m.n);
+    }
+    if (!FULL) pad<D>(g, g.h, g.h_sb, g.h_sr, m, p0);
+    if (m.sub == kSub - 1) after_tile<SPREAD>(g, m, g.h_last, s);
+}
+
+template <class D, bool SPREAD>
+__global__ __launch_bounds__(kThreads, 4) void k_tokens_fwd(Args g, bool rev) {
+    __shared__ FwdShared sh;
+    const Me m = me_of(g, my_unit<SPREAD>(g, &sh.unit));
+    const size_t at = size_t(m.b) * g.C + m.c;
+    const int p0 = m.m * kTile + m.sub * kLen;
+    if (m.m >= m.valid) {  // padding only
+        if (m.m == 0 && m.sub == 0 && g.h_last)
+            store_row(g.h_last + at, m, load_row(g.h0 ? g.h0 + at : nullptr, m));
+        pad<D>(g, g.h, g.h_sb, g.h_sr, m, p0);
+        return;
+    }
+    if (full_tile(g, m, m.m)) tile_fwd<D, SPREAD, true>(g, m, rev, sh);
+    else tile_fwd<D, SPREAD, false>(g, m, rev, sh);
+}
+
+struct BwdShared {
+    Two part[kSub][kLanes];      // maps of h
+    float2 upart[kSub][kLanes];  // and of u (the factors are the same)
+    Two look[kSub][kLanes];
+    unsigned unit;
+};
+
+template <class D, bool SPREAD, bool FULL>
+__device__ __forceinline__ void tile_bwd(const Args& g, const Me& m, bool rev, BwdShared& sh) {
+    using S = typename D::S;
+    auto& part = sh.part;
+    auto& upart = sh.upart;
+    const size_t at = size_t(m.b) * g.C + m.c;
+    const int n = m.valid - 1 - m.m;  // the tile
+    const int p0 = n * kTile + m.sub * kLen;
+    Raw<D, 2> qx[kLen], qr[kLen], qi[kLen], qd[kLen];
+    fetch_run<D, FULL>(qx, run_of<const S>(g.x, g.x_sb, g.x_sr, m, p0, rev), m, p0);
+    fetch_run<D, FULL>(qr, run_of<const S>(g.r, g.r_sb, g.r_sr, m, p0, rev), m, p0);
+    fetch_run<D, FULL>(qi, run_of<const S>(g.i, g.i_sb, g.i_sr, m, p0, rev), m, p0);
+    fetch_run<D, FULL>(qd, run_of<const S>(g.dh, g.dh_sb, g.dh_sr, m, p0, rev), m, p0);
+    float2 s = load_row(g.states + size_t(n) * g.B * g.C + at, m);
     float rate[2], sum[2] = {0.f, 0.f};
     rates(g, m, rate);
-    if (m.sub == 0) {
-        float2 s{0.f, 0.f};
-        if (g.dh_last && m.n > 0) s.x = g.dh_last[at];
-        if (g.dh_last && m.n > 1) s.y = g.dh_last[at + 1];
-        ustate[0][m.cl] = s;
-    }
-    for (int turn = 0; turn < g.tiles; ++turn) {
-        const int n = g.tiles - 1 - turn, side = turn & 1;
-        const int p0 = n * kTile + m.sub * kLen;
-        Raw<D, 2> qx[kLen], qr[kLen], qi[kLen], qd[kLen];
+    float a[2][kLen], hp[2][kLen], A[2], H[2], U[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        A[e] = 1.f;
+        H[e] = U[e] = 0.f;
 #pragma unroll
         for (int j = 0; j < kLen; ++j) {
-            const int k = p0 + j < m.len ? m.n : 0;
-            qx[j] = fetch2<D>(place<const S>(g.x, g.x_sb, g.x_sr, m, p0 + j, rev), k);
-            qr[j] = fetch2<D>(place<const S>(g.r, g.r_sb, g.r_sr, m, p0 + j, rev), k);
-            qi[j] = fetch2<D>(place<const S>(g.i, g.i_sb, g.i_sr, m, p0 + j, rev), k);
-            qd[j] = fetch2<D>(place<const S>(g.dh, g.dh_sb, g.dh_sr, m, p0 + j, rev), k);
-        }
-        float2 s{0.f, 0.f};
-        {
-            const float* q = g.states + size_t(n) * g.B * g.C + at;
-            if (m.n > 0) s.x = q[0];
-            if (m.n > 1) s.y = q[1];
-        }
-        float a[2][kLen], hp[2][kLen], A[2], H[2], U[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            A[e] = 1.f;
-            H[e] = U[e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < kLen; ++j) {
-                gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], hp[e][j]);
-                if (p0 + j >= m.len) {
-                    a[e][j] = 1.f;
-                    hp[e][j] = 0.f;
-                }
-                H[e] = fmaf(a[e][j], H[e], hp[e][j]);
-                A[e] *= a[e][j];
+            gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], hp[e][j]);
+            if (!FULL && p0 + j >= m.len) {
+                a[e][j] = 1.f;
+                hp[e][j] = 0.f;
             }
-#pragma unroll
-            for (int j = kLen - 1; j >= 0; --j) U[e] = a[e][j] * (qd[j].get(e) + U[e]);
-        }
-        part[side][m.sub][m.cl] = Two{A[0], H[0], A[1], H[1]};
-        upart[side][m.sub][m.cl] = float2{U[0], U[1]};
-        __syncthreads();
-        for (int k = 0; k < m.sub; ++k) {
-            const Two t = part[side][k][m.cl];
-            s.x = fmaf(t.a0, s.x, t.h0);
-            s.y = fmaf(t.a1, s.y, t.h1);
-        }
-        float2 u = ustate[side][m.cl];
-        for (int k = kSub - 1; k > m.sub; --k) {
-            const Two t = part[side][k][m.cl];
-            const float2 v = upart[side][k][m.cl];
-            u.x = fmaf(t.a0, u.x, v.x);
-            u.y = fmaf(t.a1, u.y, v.y);
+            H[e] = fmaf(a[e][j], H[e], hp[e][j]);
+            A[e] *= a[e][j];
         }
 #pragma unroll
-        for (int j = 0; j < kLen; ++j) {
-            float v = hp[0][j];
-            hp[0][j] = s.x;
-            s.x = fmaf(a[0][j], s.x, v);
-            v = hp[1][j];
-            hp[1][j] = s.y;
-            s.y = fmaf(a[1][j], s.y, v);
-        }
-#pragma unroll
-        for (int j = kLen - 1; j >= 0; --j) {
-            float ox[2], orr[2], oi[2], e;
-            const bool in = p0 + j < m.len;
-            float gt = qd[j].get(0) + u.x;
-            gate_bwd(qx[j].get(0), qr[j].get(0), qi[j].get(0), rate[0], a[0][j], hp[0][j], gt, ox[0],
-                     orr[0], oi[0], e);
-            sum[0] += in ? e : 0.f;
-            u.x = a[0][j] * gt;
-            gt = qd[j].get(1) + u.y;
-            gate_bwd(qx[j].get(1), qr[j].get(1), qi[j].get(1), rate[1], a[1][j], hp[1][j], gt, ox[1],
-                     orr[1], oi[1], e);
-            sum[1] += in ? e : 0.f;
-            u.y = a[1][j] * gt;
-            const int k = p0 + j < g.T ? m.n : 0;
-            put2<D>(place<S>(g.dx, g.dx_sb, g.dx_sr, m, p0 + j, rev), in ? ox[0] : 0.f, in ? ox[1] : 0.f, k);
-            put2<D>(place<S>(g.dr, g.dr_sb, g.dr_sr, m, p0 + j, rev), in ? orr[0] : 0.f, in ? orr[1] : 0.f, k);
-            put2<D>(place<S>(g.di, g.di_sb, g.di_sr, m, p0 + j, rev), in ? oi[0] : 0.f, in ? oi[1] : 0.f, k);
-        }
-        if (m.sub == 0) ustate[side ^ 1][m.cl] = u;
+        for (int j = kLen - 1; j >= 0; --j) U[e] = a[e][j] * (qd[j].get(e) + U[e]);
     }
-    if (m.sub == 0 && g.dh0) {
-        const float2 u = ustate[g.tiles & 1][m.cl];  // this thread's own store
-        if (m.n > 0) g.dh0[at] = u.x;
-        if (m.n > 1) g.dh0[at + 1] = u.y;
+    part[m.sub][m.cl] = Two{A[0], H[0], A[1], H[1]};
+    upart[m.sub][m.cl] = float2{U[0], U[1]};
+    float2 u = before_tile<SPREAD>(g, m, g.dh_last, sh.look, 0, [&] {
+        Two t = part[kSub - 1][m.cl];
+        t.h0 = upart[kSub - 1][m.cl].x;
+        t.h1 = upart[kSub - 1][m.cl].y;
+#pragma unroll 3
+        for (int k = kSub - 2; k >= 0; --k) {
+            const Two q = part[k][m.cl];
+            const float2 v = upart[k][m.cl];
+            t = Two{q.a0 * t.a0, fmaf(q.a0, t.h0, v.x), q.a1 * t.a1, fmaf(q.a1, t.h1, v.y)};
+        }
+        return t;
+    });
+    for (int k = 0; k < m.sub; ++k) {
+        const Two t = part[k][m.cl];
+        s.x = fmaf(t.a0, s.x, t.h0);
+        s.y = fmaf(t.a1, s.y, t.h1);
     }
-    // the sub-tiles' sums in order
+    for (int k = kSub - 1; k > m.sub; --k) {
+        const Two t = part[k][m.cl];
+        const float2 v = upart[k][m.cl];
+        u.x = fmaf(t.a0, u.x, v.x);
+        u.y = fmaf(t.a1, u.y, v.y);
+    }
+#pragma unroll
+    for (int j = 0; j < kLen; ++j) {
+        float v = hp[0][j];
+        hp[0][j] = s.x;
+        s.x = fmaf(a[0][j], s.x, v);
+        v = hp[1][j];
+        hp[1][j] = s.y;
+        s.y = fmaf(a[1][j], s.y, v);
+    }
+    const Run<S> px = run_of<S>(g.dx, g.dx_sb, g.dx_sr, m, p0, rev);
+    const Run<S> pr = run_of<S>(g.dr, g.dr_sb, g.dr_sr, m, p0, rev);
+    const Run<S> pi = run_of<S>(g.di, g.di_sb, g.di_sr, m, p0, rev);
+#pragma unroll
+    for (int j = kLen - 1; j >= 0; --j) {
+        float ox[2], orr[2], oi[2], e;
+        const bool in = FULL || p0 + j < m.len;
+        float gt = qd[j].get(0) + u.x;
+        gate_bwd(qx[j].get(0), qr[j].get(0), qi[j].get(0), rate[0], a[0][j], hp[0][j], gt, ox[0],
+                 orr[0], oi[0], e);
+        sum[0] += in ? e : 0.f;
+        u.x = a[0][j] * gt;
+        gt = qd[j].get(1) + u.y;
+        gate_bwd(qx[j].get(1), qr[j].get(1), qi[j].get(1), rate[1], a[1][j], hp[1][j], gt, ox[1],
+                 orr[1], oi[1], e);
+        sum[1] += in ? e : 0.f;
+        u.y = a[1][j] * gt;
+        const int k = FULL ? 2 : in ? m.n : 0;
+        put2<D>(px.at(j), ox[0], ox[1], k);
+        put2<D>(pr.at(j), orr[0], orr[1], k);
+        put2<D>(pi.at(j), oi[0], oi[1], k);
+    }
+    if (!FULL) {
+        pad<D>(g, g.dx, g.dx_sb, g.dx_sr, m, p0);
+        pad<D>(g, g.dr, g.dr_sb, g.dr_sr, m, p0);
+        pad<D>(g, g.di, g.di_sb, g.di_sr, m, p0);
+    }
+    if (m.sub == 0) after_tile<SPREAD>(g, m, g.dh0, u);
+    // the threads' sums in order
     __syncthreads();
-    upart[0][m.sub][m.cl] = float2{sum[0], sum[1]};
+    upart[m.sub][m.cl] = float2{sum[0], sum[1]};
     __syncthreads();
     if (m.sub == 0) {
-        float2 t = upart[0][0][m.cl];
+        float2 t = upart[0][m.cl];
         for (int k = 1; k < kSub; ++k) {
-            t.x += upart[0][k][m.cl].x;
-            t.y += upart[0][k][m.cl].y;
+            t.x += upart[k][m.cl].x;
+            t.y += upart[k][m.cl].y;
         }
-        if (m.n > 0) g.part[at] = t.x;
-        if (m.n > 1) g.part[at + 1] = t.y;
+        store_row(g.part + size_t(m.m) * g.B * g.C + at, m, t);
     }
+}
+
+template <class D, bool SPREAD>
+__global__ __launch_bounds__(kThreads, 4) void k_tokens_bwd(Args g, bool rev) {
+    __shared__ BwdShared sh;
+    const Me m = me_of(g, my_unit<SPREAD>(g, &sh.unit));
+    const size_t at = size_t(m.b) * g.C + m.c;
+    if (m.m >= m.valid) {
+        if (m.sub == 0) {
+            if (m.m == 0 && g.dh0) store_row(g.dh0 + at, m, load_row(g.dh_last ? g.dh_last + at : nullptr, m));
+            store_row(g.part + size_t(m.m) * g.B * g.C + at, m, float2{0.f, 0.f});
+        }
+        const int p0 = m.m * kTile + m.sub * kLen;
+        pad<D>(g, g.dx, g.dx_sb, g.dx_sr, m, p0);
+        pad<D>(g, g.dr, g.dr_sb, g.dr_sr, m, p0);
+        pad<D>(g, g.di, g.di_sb, g.di_sr, m, p0);
+        return;
+    }
+    if (full_tile(g, m, m.valid - 1 - m.m)) tile_bwd<D, SPREAD, true>(g, m, rev, sh);
+    else tile_bwd<D, SPREAD, false>(g, m, rev, sh);
 }
 
 // 16 channels by 32 threads along the rows of partial sums; the threads' sums
@@ -322,9 +481,14 @@ __global__ __launch_bounds__(256) void k_step(int C, int S, const typename D::S*
 
 template <class D>
 void launch(bool bwd, bool rev, const Args& a, hipStream_t st) {
-    const dim3 grid((a.C + kChan - 1) / kChan * unsigned(a.B));
-    if (bwd) k_tokens_bwd<D><<<grid, kThreads, 0, st>>>(a, rev);
-    else k_tokens_fwd<D><<<grid, kThreads, 0, st>>>(a, rev);
+    const dim3 grid((a.C + kChan - 1) / kChan * unsigned(a.B) * unsigned(a.tiles));
+    if (a.tiles == 1) {
+        if (bwd) k_tokens_bwd<D, false><<<grid, kThreads, 0, st>>>(a, rev);
+        else k_tokens_fwd<D, false><<<grid, kThreads, 0, st>>>(a, rev);
+    } else {
+        if (bwd) k_tokens_bwd<D, true><<<grid, kThreads, 0, st>>>(a, rev);
+        else k_tokens_fwd<D, true><<<grid, kThreads, 0, st>>>(a, rev);
+    }
 }
 void launch_type(int dtype, bool bwd, bool rev, const Args& a, hipStream_t st) {
     if (dtype == GSCAN_F32) launch<F32>(bwd, rev, a, st);
@@ -332,30 +496,59 @@ void launch_type(int dtype, bool bwd, bool rev, const Args& a, hipStream_t st) {
     else launch<BF16>(bwd, rev, a, st);
 }
 
+__global__ __launch_bounds__(256) void k_clear(uint4* p, size_t n) {
+    const size_t k = size_t(blockIdx.x) * 256 + threadIdx.x;
+    const unsigned v = k < 4 ? 0u : ~0u;  // the counter's 64 bytes
+    if (k < n) p[k] = uint4{v, v, v, v};
+}
+
+size_t tokens_carry(const gscan_shape& s, int tiles) {
+    return tiles > 1 ? carry_bytes(size_t(s.B) * s.C, tiles) : 0;
+}
+
 }  // namespace
+
+hipError_t clear_carry(void* ws, size_t bytes, hipStream_t st) {
+    const size_t n = bytes / sizeof(uint4);
+    k_clear<<<dim3((n + 255) / 256), 256, 0, st>>>(static_cast<uint4*>(ws), n);
+    return hipGetLastError();
+}
 
 Plan tokens_plan(const gscan_shape& s) {
     Plan p;
     p.tiles = s.T > 0 ? (s.T - 1) / kTile + 1 : 1;
-    p.parts = s.B;
+    p.parts = p.tiles * s.B;
     p.states = sizeof(float) * size_t(p.tiles) * s.B * s.C;
-    p.scratch = sizeof(float) * size_t(p.parts) * s.C;
+    p.scratch = tokens_carry(s, p.tiles) + sizeof(float) * size_t(p.parts) * s.C;
     return p;
 }
 
-hipError_t tokens_fwd(const gscan_shape& s, Args a, void*, hipStream_t st) {
-    a.tiles = tokens_plan(s).tiles;
-    launch_type(s.dtype, false, s.reverse != 0, a, st);
+namespace {
+
+// The words between tiles come first in the workspace, then the partial sums.
+hipError_t tokens_run(const gscan_shape& s, bool bwd, Args& a, void* ws, hipStream_t st) {
+    const Plan p = tokens_plan(s);
+    const size_t words = tokens_carry(s, p.tiles);
+    a.tiles = p.tiles;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + words);
+    if (words) {
+        a.carry = carry_at(ws, size_t(s.B) * s.C, p.tiles);
+        const hipError_t e = clear_carry(ws, words, st);
+        if (e != hipSuccess) return e;
+    }
+    launch_type(s.dtype, bwd, s.reverse != 0, a, st);
     return hipGetLastError();
 }
 
+}  // namespace
+
+hipError_t tokens_fwd(const gscan_shape& s, Args a, void* ws, hipStream_t st) {
+    return tokens_run(s, false, a, ws, st);
+}
+
 hipError_t tokens_bwd(const gscan_shape& s, Args a, void* ws, hipStream_t st) {
-    const Plan p = tokens_plan(s);
-    a.tiles = p.tiles;
-    a.part = static_cast<float*>(ws);
-    launch_type(s.dtype, true, s.reverse != 0, a, st);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? close_dlam(a, p.parts, st) : e;
+    const hipError_t e = tokens_run(s, true, a, ws, st);
+    return e == hipSuccess ? close_dlam(a, tokens_plan(s).parts, st) : e;
 }
 
 hipError_t close_dlam(const Args& a, int parts, hipStream_t st) {
