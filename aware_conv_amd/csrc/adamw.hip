@@ -68,12 +68,7 @@ __device__ __forceinline__ Raw<D, kVec> fetch(const typename D::S* p, int n) {
 template <class D>
 __device__ __forceinline__ void put(typename D::S* p, const float (&v)[kVec], int n) {
     if (n >= kVec) {
-        Raw<D, kVec> q;
-#pragma unroll
-        for (int k = 0; k < Raw<D, kVec>::kWords; ++k) q.w[k] = 0;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) q.set(j, v[j]);
-        gsc::store_vec<D, kVec>(p, q);
+        gsc::store_vec<D, kVec>(p, gsc::pack<D, false>(v));
     } else {
 #pragma unroll
         for (int j = 0; j < kVec; ++j)

@@ -12,7 +12,8 @@
 //
 // Every wait ends.  Units of work are handed out by a counter, in an order in
 // which every tile comes after the tiles that it waits for, so those are held
-// by workgroups that already run.  A map is published without waiting for
+// by workgroups that already run; one that takes several at a time works them
+// off in that order.  A map is published without waiting for
 // anything; a group's start waits for maps and the group's start before it:
 // by induction over the order, all are published.
 //
@@ -31,13 +32,18 @@ namespace gsc {
 constexpr int kGroup = 16;  // tiles per group
 
 struct Carry {
-    unsigned* next;            // units handed out
+    unsigned* next;            // shares of units handed out
+    unsigned units, share;     // all units; units of a share
     unsigned long long* maps;  // (A, H) of each tile
     unsigned* starts;          // state at the start of each group but the first
 };
 
-__device__ __forceinline__ unsigned take_unit(const Carry& c) {
-    return __hip_atomic_fetch_add(c.next, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// First unit of the workgroup's share; `shared` is a word of LDS.
+__device__ __forceinline__ unsigned take_share(const Carry& c, unsigned* shared) {
+    if (threadIdx.x == 0)
+        *shared = c.share * __hip_atomic_fetch_add(c.next, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return *shared;
 }
 
 __device__ __forceinline__ void publish_map(unsigned long long* p, float a, float h) {
@@ -64,13 +70,19 @@ inline size_t carry_bytes(size_t rows, int tiles) {
     const size_t groups = (tiles + kGroup - 1) / kGroup;
     return 64 + (sizeof(unsigned long long) * rows * tiles + sizeof(unsigned) * rows * groups + 63) / 64 * 64;
 }
-inline Carry carry_at(void* ws, size_t rows, int tiles) {
+// The counter gives out one share in about 12 ns (one address, all XCDs), so
+// units that take a workgroup little time are handed out up to `most` at
+// once, as long as that leaves a few thousand shares to balance.
+inline Carry carry_at(void* ws, size_t rows, int tiles, unsigned units, unsigned most) {
     Carry c;
+    c.units = units;
+    c.share = units / 4096 < 1 ? 1 : units / 4096 > most ? most : units / 4096;
     c.next = static_cast<unsigned*>(ws);
     c.maps = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + 64);
     c.starts = reinterpret_cast<unsigned*>(c.maps + rows * tiles);
     return c;
 }
+inline unsigned shares(const Carry& c) { return (c.units + c.share - 1) / c.share; }
 // Sets the words to "not there" and the counter to 0.
 hipError_t clear_carry(void* ws, size_t bytes, hipStream_t st);
 

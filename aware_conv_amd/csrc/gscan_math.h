@@ -25,24 +25,27 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 __device__ __forceinline__ float sqrt_hw(float x) { return __builtin_amdgcn_sqrtf(x); }
 __device__ __forceinline__ float rsq_hw(float x) { return __builtin_amdgcn_rsqf(x); }
 
-// Storage types.  Two 16-bit values share a 32-bit word, the first low.
+// Storage types.  Two 16-bit values share a 32-bit word, the first low;
+// narrowing is to nearest even (fp16: overflow to infinity).
+typedef float Float2 __attribute__((ext_vector_type(2)));
 struct F32 {
     using S = float;
     static constexpr int kBytes = 4;
 };
 struct F16 {
     using S = uint16_t;
+    using Pair = _Float16 __attribute__((ext_vector_type(2)));
     static constexpr int kBytes = 2;
     __device__ static float widen(uint32_t lo16) {
         return float(__builtin_bit_cast(_Float16, uint16_t(lo16)));
     }
-    // to nearest even, overflow to infinity
     __device__ static uint32_t narrow(float v) {
         return __builtin_bit_cast(uint16_t, _Float16(v));
     }
 };
 struct BF16 {
     using S = uint16_t;
+    using Pair = __bf16 __attribute__((ext_vector_type(2)));
     static constexpr int kBytes = 2;
     __device__ static float widen(uint32_t lo16) { return __builtin_bit_cast(float, lo16 << 16); }
     __device__ static uint32_t narrow(float v) {
@@ -73,6 +76,23 @@ struct Raw {
         }
     }
 };
+
+// The values v (V even), last first if TURNED.
+template <class D, bool TURNED, int V>
+__device__ __forceinline__ Raw<D, V> pack(const float (&v)[V]) {
+    Raw<D, V> q;
+    if constexpr (D::kBytes == 4) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) q.w[j] = __builtin_bit_cast(uint32_t, v[TURNED ? V - 1 - j : j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const Float2 f{v[TURNED ? V - 1 - j : j], v[TURNED ? V - 2 - j : j + 1]};
+            q.w[j / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, typename D::Pair));
+        }
+    }
+    return q;
+}
 
 // Any element alignment is taken: global accesses of gfx950 need none, so a
 // packed struct keeps them one wide instruction where the address is odd too.
@@ -107,65 +127,61 @@ __device__ __forceinline__ void store_one(typename D::S* p, float v) {
     else *p = typename D::S(D::narrow(v));
 }
 
-// softplus without overflow; once per row or channel and workgroup
-__device__ __forceinline__ float softplus(float v) {
-    return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
-}
-
-// 1 - a^2 = -expm1(y) for y = 2 L <= 0.  Near 0 the first eight terms of the
-// series (the ninth is below 2^-25 of the sum there); beyond, 1 - a^2 loses
-// no more than a bit.
-__device__ __forceinline__ float one_minus_sq(float a, float y) {
-    float s = fmaf(y, 1.f / 40320.f, 1.f / 5040.f);
-    s = fmaf(y, s, 1.f / 720.f);
-    s = fmaf(y, s, 1.f / 120.f);
-    s = fmaf(y, s, 1.f / 24.f);
-    s = fmaf(y, s, 1.f / 6.f);
-    s = fmaf(y, s, 0.5f);
+// decay * softplus(lam) * log2(e): the factor of sig(r) in -log2(a).
+// softplus = max(lam, 0) + log1p(e) with e = exp(-|lam|) in (0, 1], by
+// log1p(e) = 2 atanh(z), z = e / (2 + e) <= 1/3, and the series of atanh to
+// z^15 (the next term is below 2^-26 of the sum).  The library's log1pf takes
+// 120 instructions, which a thread spreads over as few as 4 elements of 45.
+__device__ __forceinline__ float rate_of(float decay, float lam) {
+    const float e = exp2_hw(-kLog2e * fabsf(lam));
+    const float z = e * rcp_hw(2.f + e), y = z * z;
+    float s = fmaf(y, 1.f / 15.f, 1.f / 13.f);
+    s = fmaf(y, s, 1.f / 11.f);
+    s = fmaf(y, s, 1.f / 9.f);
+    s = fmaf(y, s, 1.f / 7.f);
+    s = fmaf(y, s, 1.f / 5.f);
+    s = fmaf(y, s, 1.f / 3.f);
     s = fmaf(y, s, 1.f);
-    return y > -0.5f ? -y * s : fmaf(-a, a, 1.f);
+    return decay * kLog2e * (fmaxf(lam, 0.f) + 2.f * z * s);
 }
 
-// What the recurrence needs of an element: h = a h + b.  `rate` is
-// decay * softplus(lam) * log2(e), so that exp2 takes rate * sig(r) directly.
+// 1 - a^2 = 1 - 2^(2 l) for l = log2(a) <= 0.  Near 0, l times the polynomial
+// that interpolates (1 - 2^(2 l)) / l at the Chebyshev nodes of -0.25..0
+// (2^-23 off at most in fp32); beyond, a^2 is below 0.71 and the difference
+// loses no more than two bits.
+__device__ __forceinline__ float one_minus_sq(float a, float l) {
+    float s = fmaf(l, -0.03698064f, -0.15267968f);
+    s = fmaf(l, s, -0.44392628f);
+    s = fmaf(l, s, -0.96090275f);
+    s = fmaf(l, s, -1.38629436f);
+    return l > -0.25f ? l * s : fmaf(-a, a, 1.f);
+}
+
+__device__ __forceinline__ float sig(float v) { return rcp_hw(1.f + exp2_hw(-kLog2e * v)); }
+
+// What the recurrence needs of an element: h = a h + b; and its gates.
 __device__ __forceinline__ void gate_fwd(float x, float r, float i, float rate, float& a,
-                                         float& b) {
-    const float sr = rcp_hw(1.f + exp2_hw(-kLog2e * r));
-    const float l2 = -rate * sr;
-    a = exp2_hw(l2);
-    const float w = sqrt_hw(one_minus_sq(a, (2.f * kLn2) * l2));
-    const float si = rcp_hw(1.f + exp2_hw(-kLog2e * i));
-    b = w * (si * x);
+                                         float& b, float& sr, float& si) {
+    sr = sig(r);
+    si = sig(i);
+    const float l = -rate * sr;
+    a = exp2_hw(l);
+    b = sqrt_hw(one_minus_sq(a, l)) * (si * x);
 }
 
-// sig(v) and sig(-v), each accurate where it is small
-__device__ __forceinline__ void sig_both(float v, float& s, float& n) {
-    const float e = exp2_hw(-kLog2e * fabsf(v));
-    const float d = rcp_hw(1.f + e);
-    const float ed = e * d;
-    s = v >= 0.f ? d : ed;
-    n = v >= 0.f ? ed : d;
-}
-
-// Gradients of one element: g is that of h_t, hp is h_{t-1}, a as formed by
-// gate_fwd.  `e` returns e_t sig(r_t), the term of dlam.
-__device__ __forceinline__ void gate_bwd(float x, float r, float i, float rate, float a, float hp,
+// Gradients of one element from its gates and a as gate_fwd formed them: g is
+// that of h_t, hp is h_{t-1}.  `e` returns e_t sig(r_t), the term of dlam.
+__device__ __forceinline__ void gate_bwd(float x, float sr, float si, float rate, float a, float hp,
                                          float g, float& dx, float& dr, float& di, float& e) {
-    float sr, nr, si, ni;
-    sig_both(r, sr, nr);
-    sig_both(i, si, ni);
-    const float L = -kLn2 * rate * sr;
-    const float q = one_minus_sq(a, 2.f * L);
-    // 1 / w; 0 where w is 0 or its square below the normal range (v_rsq_f32
-    // would give infinity there), NaN where q is
-    const float inv = q >= 1.17549435e-38f ? rsq_hw(q) : q * 0.f;
-    const float w = q * inv;
+    const float q = one_minus_sq(a, -rate * sr);
+    // 1 / w, kept finite where q is 0 or leaves the normal range: its factors
+    // in the gradients are below 2^-60 there, and w = q inv is 0
+    const float inv = rsq_hw(q + 1.2e-37f);
     const float gx = g * si;
-    dx = gx * w;
-    di = dx * (x * ni);
-    const float d = g * (a * hp) - gx * x * (a * a * inv);
-    dr = d * L * nr;
-    e = d * sr;
+    dx = gx * (q * inv);
+    di = dx * (x * (1.f - si));
+    e = (g * (a * hp) - gx * x * (a * a * inv)) * sr;
+    dr = e * ((-kLn2 * rate) * (1.f - sr));
 }
 
 }  // namespace gsc

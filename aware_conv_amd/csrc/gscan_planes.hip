@@ -4,8 +4,12 @@
 // LW * V positions: each lane takes V consecutive ones, composes their maps
 // h -> a h + b in registers, the lanes' compositions are scanned with DPP
 // moves (no LDS), and each lane runs its V steps again from the state that it
-// then knows.  The state passes from tile to tile in a register.  Everything
-// is read once and written once.
+// then knows.  Everything is read once and written once.
+//
+// Where there are rows enough to fill the device, lanes walk the tiles of
+// their row and the state passes in a register.  Where there are few and they
+// are long, a tile is kWide positions of a workgroup, its wavefronts' maps
+// meet in LDS, and the state passes between workgroups (gscan_carry.h).
 //
 // Backwards the same tile gives h (from the state the forward kept for it)
 // and, for the sequence u_t = a_t g_t that passes from position to position,
@@ -80,10 +84,10 @@ __device__ __forceinline__ float lane_sum(float v) {
 }
 
 // Positions p0 .. p0 + V - 1 of a row in scan order, `len` of them valid.
-// REV: position p lies at len - 1 - p.
-template <class D, int V, bool REV>
+// REV: position p lies at len - 1 - p.  FULL: all V are valid.
+template <class D, int V, bool REV, bool FULL>
 __device__ __forceinline__ void fetch(Raw<D, V>& out, const typename D::S* row, int p0, int len) {
-    if (p0 + V <= len) {
+    if (FULL || p0 + V <= len) {
         load_vec<D, V>(out, row + (REV ? len - V - p0 : p0));
     } else {
 #pragma unroll
@@ -95,16 +99,11 @@ __device__ __forceinline__ void fetch(Raw<D, V>& out, const typename D::S* row, 
 }
 // The same positions written; those in len .. T - 1 (which lie at their own
 // index in both directions) become zero.
-template <class D, int V, bool REV>
+template <class D, int V, bool REV, bool FULL>
 __device__ __forceinline__ void put(typename D::S* row, const float (&v)[V], int p0, int len,
                                     int T) {
-    if (p0 + V <= len) {
-        Raw<D, V> q;
-#pragma unroll
-        for (int k = 0; k < Raw<D, V>::kWords; ++k) q.w[k] = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) q.set(REV ? V - 1 - j : j, v[j]);
-        store_vec<D, V>(row + (REV ? len - V - p0 : p0), q);
+    if (FULL || p0 + V <= len) {
+        store_vec<D, V>(row + (REV ? len - V - p0 : p0), pack<D, REV>(v));
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -127,138 +126,177 @@ __device__ __forceinline__ S* row_of(const void* p, long long sb, long long sr, 
 struct Row {
     int b, c, len;
     long long id;  // b * C + c
-    bool live;
 };
-template <int LW>
-__device__ __forceinline__ Row my_row(const Args& g) {
+__device__ __forceinline__ Row row_at(const Args& g, long long id) {
     Row w;
-    const long long rows = (long long)g.B * g.C;
-    w.id = (long long)blockIdx.x * (kThreads / LW) + threadIdx.x / LW;
-    w.live = w.id < rows;
-    const long long id = w.live ? w.id : rows - 1;
-    w.b = int(id / g.C);
-    w.c = int(id - (long long)w.b * g.C);
+    w.id = id;
+    w.b = int(unsigned(id) / unsigned(g.C));  // fewer than 2^25 rows
+    w.c = int(id) - w.b * g.C;
     w.len = g.T;
     if (g.lengths) w.len = min(max(g.lengths[w.b], 0), g.T);
     return w;
 }
 
-template <class D, int V, int LW, bool REV>
-__global__ __launch_bounds__(kThreads) void k_planes_fwd(Args g) {
+// A lane's part of a tile forwards: its elements' maps and their composition
+// (A, H), then its outputs from the state s before its first position.
+template <class D, int V, bool REV, bool FULL>
+struct Fwd {
     using S = typename D::S;
-    const Row w = my_row<LW>(g);
-    if (!w.live) return;  // whole groups of lanes
-    const long long rows = (long long)g.B * g.C;
-    const int lane = threadIdx.x % LW;
-    const S* x = row_of<const S>(g.x, g.x_sb, g.x_sr, w.b, w.c);
-    const S* r = row_of<const S>(g.r, g.r_sb, g.r_sr, w.b, w.c);
-    const S* i = row_of<const S>(g.i, g.i_sb, g.i_sr, w.b, w.c);
-    S* h = row_of<S>(g.h, g.h_sb, g.h_sr, w.b, w.c);
-    const float rate = g.decay * softplus(g.lam[w.c]) * kLog2e;
-    float carry = g.h0 ? g.h0[w.id] : 0.f;
-    for (int n = 0; n < g.tiles; ++n) {
-        const int p0 = (n * LW + lane) * V;
-        if (g.states && lane == 0) g.states[n * rows + w.id] = carry;
+    float a[V], b[V], A, H;
+    __device__ __forceinline__ void open(const Args& g, const Row& w, int p0, float rate) {
         Raw<D, V> qx, qr, qi;
-        fetch<D, V, REV>(qx, x, p0, w.len);
-        fetch<D, V, REV>(qr, r, p0, w.len);
-        fetch<D, V, REV>(qi, i, p0, w.len);
-        float a[V], b[V];
-        float A = 1.f, H = 0.f;
+        fetch<D, V, REV, FULL>(qx, row_of<const S>(g.x, g.x_sb, g.x_sr, w.b, w.c), p0, w.len);
+        fetch<D, V, REV, FULL>(qr, row_of<const S>(g.r, g.r_sb, g.r_sr, w.b, w.c), p0, w.len);
+        fetch<D, V, REV, FULL>(qi, row_of<const S>(g.i, g.i_sb, g.i_sr, w.b, w.c), p0, w.len);
+        A = 1.f;
+        H = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+            float sr, si;
             gate_fwd(at<D, V, REV>(qx, j), at<D, V, REV>(qr, j), at<D, V, REV>(qi, j), rate, a[j],
-                     b[j]);
-            if (p0 + j >= w.len) {
+                     b[j], sr, si);
+            if (!FULL && p0 + j >= w.len) {
                 a[j] = 1.f;
                 b[j] = 0.f;
             }
             H = fmaf(a[j], H, b[j]);
             A *= a[j];
         }
-        lane_scan<LW>(A, H);
-        float s = fmaf(lane_before<LW>(A, 1.f), carry, lane_before<LW>(H, 0.f));
-        carry = fmaf(lane_last<LW>(A), carry, lane_last<LW>(H));
+    }
+    __device__ __forceinline__ void close(const Args& g, const Row& w, int p0, float s) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             s = fmaf(a[j], s, b[j]);
             b[j] = s;
         }
-        put<D, V, REV>(h, b, p0, w.len, g.T);
+        put<D, V, REV, FULL>(row_of<S>(g.h, g.h_sb, g.h_sr, w.b, w.c), b, p0, w.len, g.T);
+    }
+};
+
+// Backwards: the maps of h (A, H) and of u (A, U) of its elements, then its
+// outputs from the state s before its first position and u after its last.
+template <class D, int V, bool REV, bool FULL>
+struct Bwd {
+    using S = typename D::S;
+    Raw<D, V> qx, qd;
+    float sr[V], si[V], a[V], b[V], A, H, U;
+    __device__ __forceinline__ void open(const Args& g, const Row& w, int p0, float rate) {
+        Raw<D, V> qr, qi;
+        fetch<D, V, REV, FULL>(qx, row_of<const S>(g.x, g.x_sb, g.x_sr, w.b, w.c), p0, w.len);
+        fetch<D, V, REV, FULL>(qr, row_of<const S>(g.r, g.r_sb, g.r_sr, w.b, w.c), p0, w.len);
+        fetch<D, V, REV, FULL>(qi, row_of<const S>(g.i, g.i_sb, g.i_sr, w.b, w.c), p0, w.len);
+        fetch<D, V, REV, FULL>(qd, row_of<const S>(g.dh, g.dh_sb, g.dh_sr, w.b, w.c), p0, w.len);
+        A = 1.f;
+        H = U = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            gate_fwd(at<D, V, REV>(qx, j), at<D, V, REV>(qr, j), at<D, V, REV>(qi, j), rate, a[j],
+                     b[j], sr[j], si[j]);
+            if (!FULL && p0 + j >= w.len) {
+                a[j] = 1.f;
+                b[j] = 0.f;
+            }
+            H = fmaf(a[j], H, b[j]);
+            A *= a[j];
+        }
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j) U = a[j] * (at<D, V, REV>(qd, j) + U);
+    }
+    // returns the lane's part of the sum for dlam
+    __device__ __forceinline__ float close(const Args& g, const Row& w, int p0, float rate, float s,
+                                           float u) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float v = b[j];
+            b[j] = s;
+            s = fmaf(a[j], s, v);
+        }
+        float ox[V], orr[V], oi[V], sum = 0.f;
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j) {
+            const float gt = at<D, V, REV>(qd, j) + u;
+            float e;
+            gate_bwd(at<D, V, REV>(qx, j), sr[j], si[j], rate, a[j], b[j], gt, ox[j], orr[j], oi[j], e);
+            sum += FULL || p0 + j < w.len ? e : 0.f;
+            u = a[j] * gt;
+        }
+        put<D, V, REV, FULL>(row_of<S>(g.dx, g.dx_sb, g.dx_sr, w.b, w.c), ox, p0, w.len, g.T);
+        put<D, V, REV, FULL>(row_of<S>(g.dr, g.dr_sb, g.dr_sr, w.b, w.c), orr, p0, w.len, g.T);
+        put<D, V, REV, FULL>(row_of<S>(g.di, g.di_sb, g.di_sr, w.b, w.c), oi, p0, w.len, g.T);
+        return sum;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// a group of lanes walks its row
+// ---------------------------------------------------------------------------
+
+template <int LW>
+__device__ __forceinline__ bool my_row(const Args& g, Row& w) {
+    const long long id = (long long)blockIdx.x * (kThreads / LW) + threadIdx.x / LW;
+    if (id >= (long long)g.B * g.C) return false;  // whole groups of lanes
+    w = row_at(g, id);
+    return true;
+}
+
+template <class D, int V, int LW, bool REV, bool FULL>
+__device__ __forceinline__ void step_fwd(const Args& g, const Row& w, int p0, float rate,
+                                         float& carry) {
+    Fwd<D, V, REV, FULL> t;
+    t.open(g, w, p0, rate);
+    lane_scan<LW>(t.A, t.H);
+    const float s = fmaf(lane_before<LW>(t.A, 1.f), carry, lane_before<LW>(t.H, 0.f));
+    carry = fmaf(lane_last<LW>(t.A), carry, lane_last<LW>(t.H));
+    t.close(g, w, p0, s);
+}
+
+template <class D, int V, int LW, bool REV>
+__global__ __launch_bounds__(kThreads) void k_planes_fwd(Args g) {
+    Row w;
+    if (!my_row<LW>(g, w)) return;
+    const long long rows = (long long)g.B * g.C;
+    const int lane = threadIdx.x % LW;
+    const float rate = rate_of(g.decay, g.lam[w.c]);
+    float carry = g.h0 ? g.h0[w.id] : 0.f;
+    for (int n = 0; n < g.tiles; ++n) {
+        const int p0 = (n * LW + lane) * V;
+        if (g.states && lane == 0) g.states[n * rows + w.id] = carry;
+        if (LW == 64 && (n + 1) * LW * V <= w.len) step_fwd<D, V, LW, REV, true>(g, w, p0, rate, carry);
+        else step_fwd<D, V, LW, REV, false>(g, w, p0, rate, carry);
     }
     if (g.h_last && lane == 0) g.h_last[w.id] = carry;
 }
 
+template <class D, int V, int LW, bool REV, bool FULL>
+__device__ __forceinline__ float step_bwd(const Args& g, const Row& w, int p0, float rate,
+                                          float state, float& after) {
+    Bwd<D, V, REV, FULL> t;
+    t.open(g, w, p0, rate);
+    float B = lane_mirror<LW>(t.A), U = lane_mirror<LW>(t.U);
+    lane_scan<LW>(t.A, t.H);
+    const float s = fmaf(lane_before<LW>(t.A, 1.f), state, lane_before<LW>(t.H, 0.f));
+    lane_scan<LW>(B, U);
+    const float u = fmaf(lane_mirror<LW>(lane_before<LW>(B, 1.f)), after,
+                         lane_mirror<LW>(lane_before<LW>(U, 0.f)));
+    after = fmaf(lane_last<LW>(B), after, lane_last<LW>(U));
+    return t.close(g, w, p0, rate, s, u);
+}
+
 template <class D, int V, int LW, bool REV>
 __global__ __launch_bounds__(kThreads) void k_planes_bwd(Args g) {
-    using S = typename D::S;
-    const Row w = my_row<LW>(g);
-    if (!w.live) return;
+    Row w;
+    if (!my_row<LW>(g, w)) return;
     const long long rows = (long long)g.B * g.C;
     const int lane = threadIdx.x % LW;
-    const S* x = row_of<const S>(g.x, g.x_sb, g.x_sr, w.b, w.c);
-    const S* r = row_of<const S>(g.r, g.r_sb, g.r_sr, w.b, w.c);
-    const S* i = row_of<const S>(g.i, g.i_sb, g.i_sr, w.b, w.c);
-    const S* dh = row_of<const S>(g.dh, g.dh_sb, g.dh_sr, w.b, w.c);
-    S* dx = row_of<S>(g.dx, g.dx_sb, g.dx_sr, w.b, w.c);
-    S* dr = row_of<S>(g.dr, g.dr_sb, g.dr_sr, w.b, w.c);
-    S* di = row_of<S>(g.di, g.di_sb, g.di_sr, w.b, w.c);
-    const float rate = g.decay * softplus(g.lam[w.c]) * kLog2e;
+    const float rate = rate_of(g.decay, g.lam[w.c]);
     float after = g.dh_last ? g.dh_last[w.id] : 0.f;  // u of the position after the tile
     float sum = 0.f;
     for (int n = g.tiles - 1; n >= 0; --n) {
         const int p0 = (n * LW + lane) * V;
-        Raw<D, V> qx, qr, qi, qd;
-        fetch<D, V, REV>(qx, x, p0, w.len);
-        fetch<D, V, REV>(qr, r, p0, w.len);
-        fetch<D, V, REV>(qi, i, p0, w.len);
-        fetch<D, V, REV>(qd, dh, p0, w.len);
-        const float carry = g.states[n * rows + w.id];
-        float a[V], hp[V], d[V];
-        float A = 1.f, H = 0.f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            gate_fwd(at<D, V, REV>(qx, j), at<D, V, REV>(qr, j), at<D, V, REV>(qi, j), rate, a[j],
-                     hp[j]);
-            if (p0 + j >= w.len) {
-                a[j] = 1.f;
-                hp[j] = 0.f;
-            }
-            d[j] = at<D, V, REV>(qd, j);
-            H = fmaf(a[j], H, hp[j]);
-            A *= a[j];
-        }
-        float B = A, U = 0.f;
-#pragma unroll
-        for (int j = V - 1; j >= 0; --j) U = a[j] * (d[j] + U);
-        lane_scan<LW>(A, H);
-        float s = fmaf(lane_before<LW>(A, 1.f), carry, lane_before<LW>(H, 0.f));
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float b = hp[j];
-            hp[j] = s;
-            s = fmaf(a[j], s, b);
-        }
-        B = lane_mirror<LW>(B);
-        U = lane_mirror<LW>(U);
-        lane_scan<LW>(B, U);
-        const float Bb = lane_mirror<LW>(lane_before<LW>(B, 1.f));
-        const float Ub = lane_mirror<LW>(lane_before<LW>(U, 0.f));
-        float u = fmaf(Bb, after, Ub);
-        after = fmaf(lane_last<LW>(B), after, lane_last<LW>(U));
-        float ox[V], orr[V], oi[V];
-#pragma unroll
-        for (int j = V - 1; j >= 0; --j) {
-            const float gt = d[j] + u;
-            float e;
-            gate_bwd(at<D, V, REV>(qx, j), at<D, V, REV>(qr, j), at<D, V, REV>(qi, j), rate, a[j],
-                     hp[j], gt, ox[j], orr[j], oi[j], e);
-            sum += p0 + j < w.len ? e : 0.f;
-            u = a[j] * gt;
-        }
-        put<D, V, REV>(dx, ox, p0, w.len, g.T);
-        put<D, V, REV>(dr, orr, p0, w.len, g.T);
-        put<D, V, REV>(di, oi, p0, w.len, g.T);
+        const float state = g.states[n * rows + w.id];
+        if (LW == 64 && (n + 1) * LW * V <= w.len)
+            sum += step_bwd<D, V, LW, REV, true>(g, w, p0, rate, state, after);
+        else sum += step_bwd<D, V, LW, REV, false>(g, w, p0, rate, state, after);
     }
     sum = lane_sum<LW>(sum);
     if (lane == 0) {
@@ -267,16 +305,229 @@ __global__ __launch_bounds__(kThreads) void k_planes_bwd(Args g) {
     }
 }
 
-// Lanes per row and positions per lane, by the row's length alone, so that
-// the states of a forward call fit the backward one: the narrowest group that
-// holds the row in one tile, else whole wavefronts of 8 positions per lane.
+// ---------------------------------------------------------------------------
+// the tiles of a row spread over workgroups
+// ---------------------------------------------------------------------------
+
+constexpr int kWaves = kThreads / 64;
+constexpr int kWideV = 8;
+constexpr int kWide = kThreads * kWideV;  // positions of a tile
+// Units of a share: 8x64x512x512 fp32 forward 799 us one by one (the counter's
+// pace), 467 us with 8.
+constexpr unsigned kShare = 8;
+
+struct Spread {
+    float A[kWaves], H[kWaves], U[kWaves];  // maps of the wavefronts
+    float carry;
+    unsigned unit;
+};
+
+// What a workgroup works on: tile m of its row in the order of the scan.
+struct Unit {
+    Row w;
+    int m, valid;
+};
+__device__ __forceinline__ Unit unit_at(const Args& g, unsigned unit) {
+    const unsigned rows = unsigned(g.B) * unsigned(g.C);
+    Unit u;
+    u.m = unit / rows;
+    u.w = row_at(g, unit - unsigned(u.m) * rows);
+    u.valid = (u.w.len + kWide - 1) / kWide;
+    return u;
+}
+
+// The state before the unit's tile, from `first`, that before the whole scan:
+// a lane waits for each map since the group's start and they are composed
+// across lanes, always in the same order.  By one wavefront.
+__device__ __forceinline__ float await(const Args& g, const Unit& u, const float* first) {
+    const int lane = threadIdx.x & 63, grp = u.m / kGroup, k = u.m % kGroup;
+    float a = 1.f, h = 0.f;
+    if (lane < k) {
+        const unsigned long long* p = g.carry.maps + u.w.id * g.tiles + (grp * kGroup + lane);
+        unsigned long long v;
+        while ((v = peek_map(p)) == ~0ull) __builtin_amdgcn_s_sleep(1);
+        a = map_a(v);
+        h = map_h(v);
+    }
+    float s;
+    if (grp > 0) {
+        const unsigned* p = g.carry.starts + u.w.id * ((g.tiles + kGroup - 1) / kGroup) + grp;
+        unsigned v;
+        while ((v = peek_start(p)) == ~0u) __builtin_amdgcn_s_sleep(1);
+        s = __uint_as_float(v);
+    } else {
+        s = first ? first[u.w.id] : 0.f;
+    }
+    static_assert(kGroup == 16, "a group's maps lie in one row of lanes");
+    lane_scan<16>(a, h);
+    a = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, a), 15));
+    h = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, h), 15));
+    return fmaf(a, s, h);
+}
+__device__ __forceinline__ void give_map(const Args& g, const Unit& u, float a, float h) {
+    if (u.m + 1 < u.valid && u.m % kGroup != kGroup - 1)
+        publish_map(g.carry.maps + u.w.id * g.tiles + u.m, a, h);
+}
+// After the tile: the next group's start, or the end of the scan.
+__device__ __forceinline__ void give_state(const Args& g, const Unit& u, float* last, float s) {
+    if (u.m + 1 < u.valid) {
+        if (u.m % kGroup == kGroup - 1)
+            publish_start(g.carry.starts + u.w.id * ((g.tiles + kGroup - 1) / kGroup) +
+                              u.m / kGroup + 1, s);
+    } else if (last) {
+        last[u.w.id] = s;
+    }
+}
+
+// Zeros over the unit's tile, which is padding.
+template <class D>
+__device__ __forceinline__ void pad(const Args& g, const Unit& u, void* out, long long sb, long long sr) {
+    using S = typename D::S;
+    S* row = row_of<S>(out, sb, sr, u.w.b, u.w.c);
+    for (int p = u.m * kWide + threadIdx.x; p < min(g.T, (u.m + 1) * kWide); p += kThreads)
+        store_one<D>(row + p, 0.f);
+}
+
+template <class D, bool REV, bool FULL>
+__device__ __forceinline__ void spread_fwd(const Args& g, const Unit& u, Spread& sh) {
+    const int wave = threadIdx.x / 64, p0 = (u.m * kThreads + threadIdx.x) * kWideV;
+    Fwd<D, kWideV, REV, FULL> t;
+    t.open(g, u.w, p0, rate_of(g.decay, g.lam[u.w.c]));
+    lane_scan<64>(t.A, t.H);
+    if ((threadIdx.x & 63) == 63) {
+        sh.A[wave] = t.A;
+        sh.H[wave] = t.H;
+    }
+    __syncthreads();
+    if (threadIdx.x == kThreads - 1) {
+        float a = sh.A[0], h = sh.H[0];
+        for (int k = 1; k < kWaves; ++k) {
+            h = fmaf(sh.A[k], h, sh.H[k]);
+            a *= sh.A[k];
+        }
+        give_map(g, u, a, h);
+    }
+    if (wave == 0) {
+        const float s = await(g, u, g.h0);
+        if (threadIdx.x == 0) {
+            sh.carry = s;
+            if (g.states) g.states[(long long)u.m * g.B * g.C + u.w.id] = s;
+        }
+    }
+    __syncthreads();
+    float s = sh.carry;
+    for (int k = 0; k < wave; ++k) s = fmaf(sh.A[k], s, sh.H[k]);
+    if (threadIdx.x == kThreads - 1) give_state(g, u, g.h_last, fmaf(t.A, s, t.H));
+    s = fmaf(lane_before<64>(t.A, 1.f), s, lane_before<64>(t.H, 0.f));
+    t.close(g, u.w, p0, s);
+}
+
+template <class D, bool REV>
+__global__ __launch_bounds__(kThreads) void k_spread_fwd(Args g) {
+    __shared__ Spread sh;
+    const unsigned from = take_share(g.carry, &sh.unit);
+    for (unsigned k = from; k < min(from + g.carry.share, g.carry.units); ++k) {
+        const Unit u = unit_at(g, k);
+        if (u.m >= u.valid) {
+            if (u.m == 0 && threadIdx.x == 0 && g.h_last) g.h_last[u.w.id] = g.h0 ? g.h0[u.w.id] : 0.f;
+            pad<D>(g, u, g.h, g.h_sb, g.h_sr);
+        } else if ((u.m + 1) * kWide <= u.w.len) {
+            spread_fwd<D, REV, true>(g, u, sh);
+        } else {
+            spread_fwd<D, REV, false>(g, u, sh);
+        }
+        __syncthreads();
+    }
+}
+
+template <class D, bool REV, bool FULL>
+__device__ __forceinline__ void spread_bwd(const Args& g, const Unit& u, Spread& sh) {
+    const int wave = threadIdx.x / 64, n = u.valid - 1 - u.m;
+    const int p0 = (n * kThreads + threadIdx.x) * kWideV;
+    const long long rows = (long long)g.B * g.C;
+    const float rate = rate_of(g.decay, g.lam[u.w.c]);
+    float s = g.states[n * rows + u.w.id];
+    Bwd<D, kWideV, REV, FULL> t;
+    t.open(g, u.w, p0, rate);
+    float B = lane_mirror<64>(t.A), U = lane_mirror<64>(t.U);
+    lane_scan<64>(t.A, t.H);
+    lane_scan<64>(B, U);
+    if ((threadIdx.x & 63) == 63) {
+        sh.A[wave] = t.A;
+        sh.H[wave] = t.H;
+        sh.U[wave] = U;
+    }
+    __syncthreads();
+    if (threadIdx.x == kThreads - 1) {
+        float a = sh.A[kWaves - 1], h = sh.U[kWaves - 1];
+        for (int k = kWaves - 2; k >= 0; --k) {
+            h = fmaf(sh.A[k], h, sh.U[k]);
+            a *= sh.A[k];
+        }
+        give_map(g, u, a, h);
+    }
+    if (wave == 0) {
+        const float v = await(g, u, g.dh_last);
+        if (threadIdx.x == 0) sh.carry = v;
+    }
+    __syncthreads();
+    for (int k = 0; k < wave; ++k) s = fmaf(sh.A[k], s, sh.H[k]);
+    s = fmaf(lane_before<64>(t.A, 1.f), s, lane_before<64>(t.H, 0.f));
+    float v = sh.carry;
+    for (int k = kWaves - 1; k > wave; --k) v = fmaf(sh.A[k], v, sh.U[k]);
+    if (threadIdx.x == 63) give_state(g, u, g.dh0, fmaf(B, v, U));
+    v = fmaf(lane_mirror<64>(lane_before<64>(B, 1.f)), v, lane_mirror<64>(lane_before<64>(U, 0.f)));
+    const float sum = lane_sum<64>(t.close(g, u.w, p0, rate, s, v));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh.U[wave] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float q = sh.U[0];
+        for (int k = 1; k < kWaves; ++k) q += sh.U[k];
+        g.part[u.m * rows + u.w.id] = q;
+    }
+}
+
+template <class D, bool REV>
+__global__ __launch_bounds__(kThreads) void k_spread_bwd(Args g) {
+    __shared__ Spread sh;
+    const unsigned from = take_share(g.carry, &sh.unit);
+    for (unsigned k = from; k < min(from + g.carry.share, g.carry.units); ++k) {
+        const Unit u = unit_at(g, k);
+        if (u.m >= u.valid) {
+            if (threadIdx.x == 0) {
+                if (u.m == 0 && g.dh0) g.dh0[u.w.id] = g.dh_last ? g.dh_last[u.w.id] : 0.f;
+                g.part[(long long)u.m * g.B * g.C + u.w.id] = 0.f;
+            }
+            pad<D>(g, u, g.dx, g.dx_sb, g.dx_sr);
+            pad<D>(g, u, g.dr, g.dr_sb, g.dr_sr);
+            pad<D>(g, u, g.di, g.di_sb, g.di_sr);
+        } else if ((u.valid - u.m) * kWide <= u.w.len) {
+            spread_bwd<D, REV, true>(g, u, sh);
+        } else {
+            spread_bwd<D, REV, false>(g, u, sh);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+// Lanes per row and positions per lane, or LW = 0: tiles spread over
+// workgroups.  By the shape alone, so that the states of a forward call fit
+// the backward one: the narrowest group that holds the row in one tile, else
+// whole wavefronts of 8 positions per lane.
+constexpr long long kFewRows = 4096;
 struct Form {
     int V, LW;
 };
-Form form_of(int T) {
-    if (T <= 4) return {4, 1};
-    if (T <= 64) return {4, 16};
-    if (T <= 256) return {4, 64};
+Form form_of(const gscan_shape& s) {
+    if (s.T <= 4) return {4, 1};
+    if (s.T <= 64) return {4, 16};
+    if (s.T <= 256) return {4, 64};
+    if (s.T > kWide && (long long)s.B * s.C < kFewRows) return {kWideV, 0};
     return {8, 64};
 }
 
@@ -294,45 +545,68 @@ void launch(bool bwd, bool rev, const Args& a, hipStream_t st) {
     }
 }
 template <class D>
-void launch_form(bool bwd, bool rev, const Args& a, hipStream_t st) {
-    const Form f = form_of(a.T);
-    if (f.LW == 1) launch<D, 4, 1>(bwd, rev, a, st);
+void launch_spread(bool bwd, bool rev, const Args& a, hipStream_t st) {
+    const dim3 grid(shares(a.carry));
+    if (bwd) {
+        if (rev) k_spread_bwd<D, true><<<grid, kThreads, 0, st>>>(a);
+        else k_spread_bwd<D, false><<<grid, kThreads, 0, st>>>(a);
+    } else {
+        if (rev) k_spread_fwd<D, true><<<grid, kThreads, 0, st>>>(a);
+        else k_spread_fwd<D, false><<<grid, kThreads, 0, st>>>(a);
+    }
+}
+template <class D>
+void launch_form(const Form& f, bool bwd, bool rev, const Args& a, hipStream_t st) {
+    if (f.LW == 0) launch_spread<D>(bwd, rev, a, st);
+    else if (f.LW == 1) launch<D, 4, 1>(bwd, rev, a, st);
     else if (f.LW == 16) launch<D, 4, 16>(bwd, rev, a, st);
     else if (f.V == 4) launch<D, 4, 64>(bwd, rev, a, st);
     else launch<D, 8, 64>(bwd, rev, a, st);
 }
-void launch_type(int dtype, bool bwd, bool rev, const Args& a, hipStream_t st) {
-    if (dtype == GSCAN_F32) launch_form<F32>(bwd, rev, a, st);
-    else if (dtype == GSCAN_F16) launch_form<F16>(bwd, rev, a, st);
-    else launch_form<BF16>(bwd, rev, a, st);
+
+size_t words_of(const gscan_shape& s, const Form& f, int tiles) {
+    return f.LW == 0 ? carry_bytes(size_t(s.B) * s.C, tiles) : 0;
+}
+
+// The words between tiles come first in the workspace, then the partial sums.
+hipError_t run(const gscan_shape& s, bool bwd, Args& a, void* ws, hipStream_t st) {
+    const Form f = form_of(s);
+    const Plan p = planes_plan(s);
+    const size_t words = words_of(s, f, p.tiles);
+    a.tiles = p.tiles;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + words);
+    if (words) {
+        a.carry = carry_at(ws, size_t(s.B) * s.C, p.tiles, unsigned(s.B) * s.C * p.tiles, kShare);
+        const hipError_t e = clear_carry(ws, words, st);
+        if (e != hipSuccess) return e;
+    }
+    const bool rev = s.reverse != 0;
+    if (s.dtype == GSCAN_F32) launch_form<F32>(f, bwd, rev, a, st);
+    else if (s.dtype == GSCAN_F16) launch_form<F16>(f, bwd, rev, a, st);
+    else launch_form<BF16>(f, bwd, rev, a, st);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 Plan planes_plan(const gscan_shape& s) {
-    const Form f = form_of(s.T);
-    const int tile = f.V * f.LW;
+    const Form f = form_of(s);
+    const int tile = f.LW == 0 ? kWide : f.V * f.LW;
     Plan p;
     p.tiles = s.T > 0 ? (s.T - 1) / tile + 1 : 1;
-    p.parts = s.B;
+    p.parts = f.LW == 0 ? p.tiles * s.B : s.B;
     p.states = sizeof(float) * size_t(p.tiles) * s.B * s.C;
-    p.scratch = sizeof(float) * size_t(p.parts) * s.C;
+    p.scratch = words_of(s, f, p.tiles) + sizeof(float) * size_t(p.parts) * s.C;
     return p;
 }
 
-hipError_t planes_fwd(const gscan_shape& s, Args a, void*, hipStream_t st) {
-    a.tiles = planes_plan(s).tiles;
-    launch_type(s.dtype, false, s.reverse != 0, a, st);
-    return hipGetLastError();
+hipError_t planes_fwd(const gscan_shape& s, Args a, void* ws, hipStream_t st) {
+    return run(s, false, a, ws, st);
 }
 
 hipError_t planes_bwd(const gscan_shape& s, Args a, void* ws, hipStream_t st) {
-    const Plan p = planes_plan(s);
-    a.tiles = p.tiles;
-    a.part = static_cast<float*>(ws);
-    launch_type(s.dtype, true, s.reverse != 0, a, st);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? close_dlam(a, p.parts, st) : e;
+    const hipError_t e = run(s, true, a, ws, st);
+    return e == hipSuccess ? close_dlam(a, planes_plan(s).parts, st) : e;
 }
 
 }  // namespace gsc

@@ -35,12 +35,8 @@ __device__ __forceinline__ Raw<D, 2> fetch2(const typename D::S* p, int n) {
 template <class D>
 __device__ __forceinline__ void put2(typename D::S* p, float v0, float v1, int n) {
     if (n == 2) {
-        Raw<D, 2> q;
-#pragma unroll
-        for (int k = 0; k < Raw<D, 2>::kWords; ++k) q.w[k] = 0;
-        q.set(0, v0);
-        q.set(1, v1);
-        store_vec<D, 2>(p, q);
+        const float v[2] = {v0, v1};
+        store_vec<D, 2>(p, pack<D, false>(v));
     } else if (n == 1) {
         store_one<D>(p, v0);
     }
@@ -103,8 +99,8 @@ struct Two {
 };
 
 __device__ __forceinline__ void rates(const Args& g, const Me& m, float (&rate)[2]) {
-    rate[0] = m.n > 0 ? g.decay * softplus(g.lam[m.c]) * kLog2e : 0.f;
-    rate[1] = m.n > 1 ? g.decay * softplus(g.lam[m.c + 1]) * kLog2e : 0.f;
+    rate[0] = m.n > 0 ? rate_of(g.decay, g.lam[m.c]) : 0.f;
+    rate[1] = m.n > 1 ? rate_of(g.decay, g.lam[m.c + 1]) : 0.f;
 }
 
 __device__ __forceinline__ float2 load_row(const float* p, const Me& m) {
@@ -208,14 +204,6 @@ __device__ __forceinline__ void after_tile(const Args& g, const Me& m, float* la
     }
 }
 
-template <bool SPREAD>
-__device__ __forceinline__ unsigned my_unit(const Args& g, unsigned* shared) {
-    if constexpr (!SPREAD) return blockIdx.x;
-    if (threadIdx.x == 0) *shared = take_unit(g.carry);
-    __syncthreads();
-    return *shared;
-}
-
 struct FwdShared {
     Two part[kSub][kLanes], look[kSub][kLanes];
     unsigned unit;
@@ -241,7 +229,8 @@ __device__ __forceinline__ void tile_fwd(const Args& g, const Me& m, bool rev, F
         H[e] = 0.f;
 #pragma unroll
         for (int j = 0; j < kLen; ++j) {
-            gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], b[e][j]);
+            float sr, si;
+            gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], b[e][j], sr, si);
             if (!FULL && p0 + j >= m.len) {
                 a[e][j] = 1.f;
                 b[e][j] = 0.f;
@@ -280,17 +269,17 @@ __device__ __forceinline__ void tile_fwd(const Args& g, const Me& m, bool rev, F
 template <class D, bool SPREAD>
 __global__ __launch_bounds__(kThreads, 4) void k_tokens_fwd(Args g, bool rev) {
     __shared__ FwdShared sh;
-    const Me m = me_of(g, my_unit<SPREAD>(g, &sh.unit));
-    const size_t at = size_t(m.b) * g.C + m.c;
-    const int p0 = m.m * kTile + m.sub * kLen;
+    const Me m = me_of(g, SPREAD ? take_share(g.carry, &sh.unit) : blockIdx.x);
     if (m.m >= m.valid) {  // padding only
+        const size_t at = size_t(m.b) * g.C + m.c;
         if (m.m == 0 && m.sub == 0 && g.h_last)
             store_row(g.h_last + at, m, load_row(g.h0 ? g.h0 + at : nullptr, m));
-        pad<D>(g, g.h, g.h_sb, g.h_sr, m, p0);
-        return;
+        pad<D>(g, g.h, g.h_sb, g.h_sr, m, m.m * kTile + m.sub * kLen);
+    } else if (full_tile(g, m, m.m)) {
+        tile_fwd<D, SPREAD, true>(g, m, rev, sh);
+    } else {
+        tile_fwd<D, SPREAD, false>(g, m, rev, sh);
     }
-    if (full_tile(g, m, m.m)) tile_fwd<D, SPREAD, true>(g, m, rev, sh);
-    else tile_fwd<D, SPREAD, false>(g, m, rev, sh);
 }
 
 struct BwdShared {
@@ -316,14 +305,15 @@ __device__ __forceinline__ void tile_bwd(const Args& g, const Me& m, bool rev, B
     float2 s = load_row(g.states + size_t(n) * g.B * g.C + at, m);
     float rate[2], sum[2] = {0.f, 0.f};
     rates(g, m, rate);
-    float a[2][kLen], hp[2][kLen], A[2], H[2], U[2];
+    float a[2][kLen], hp[2][kLen], sr[2][kLen], si[2][kLen], A[2], H[2], U[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         A[e] = 1.f;
         H[e] = U[e] = 0.f;
 #pragma unroll
         for (int j = 0; j < kLen; ++j) {
-            gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], hp[e][j]);
+            gate_fwd(qx[j].get(e), qr[j].get(e), qi[j].get(e), rate[e], a[e][j], hp[e][j], sr[e][j],
+                     si[e][j]);
             if (!FULL && p0 + j >= m.len) {
                 a[e][j] = 1.f;
                 hp[e][j] = 0.f;
@@ -376,13 +366,13 @@ __device__ __forceinline__ void tile_bwd(const Args& g, const Me& m, bool rev, B
         float ox[2], orr[2], oi[2], e;
         const bool in = FULL || p0 + j < m.len;
         float gt = qd[j].get(0) + u.x;
-        gate_bwd(qx[j].get(0), qr[j].get(0), qi[j].get(0), rate[0], a[0][j], hp[0][j], gt, ox[0],
-                 orr[0], oi[0], e);
+        gate_bwd(qx[j].get(0), sr[0][j], si[0][j], rate[0], a[0][j], hp[0][j], gt, ox[0], orr[0],
+                 oi[0], e);
         sum[0] += in ? e : 0.f;
         u.x = a[0][j] * gt;
         gt = qd[j].get(1) + u.y;
-        gate_bwd(qx[j].get(1), qr[j].get(1), qi[j].get(1), rate[1], a[1][j], hp[1][j], gt, ox[1],
-                 orr[1], oi[1], e);
+        gate_bwd(qx[j].get(1), sr[1][j], si[1][j], rate[1], a[1][j], hp[1][j], gt, ox[1], orr[1],
+                 oi[1], e);
         sum[1] += in ? e : 0.f;
         u.y = a[1][j] * gt;
         const int k = FULL ? 2 : in ? m.n : 0;
@@ -413,21 +403,23 @@ __device__ __forceinline__ void tile_bwd(const Args& g, const Me& m, bool rev, B
 template <class D, bool SPREAD>
 __global__ __launch_bounds__(kThreads, 4) void k_tokens_bwd(Args g, bool rev) {
     __shared__ BwdShared sh;
-    const Me m = me_of(g, my_unit<SPREAD>(g, &sh.unit));
-    const size_t at = size_t(m.b) * g.C + m.c;
+    const Me m = me_of(g, SPREAD ? take_share(g.carry, &sh.unit) : blockIdx.x);
     if (m.m >= m.valid) {
+        const size_t at = size_t(m.b) * g.C + m.c;
         if (m.sub == 0) {
-            if (m.m == 0 && g.dh0) store_row(g.dh0 + at, m, load_row(g.dh_last ? g.dh_last + at : nullptr, m));
+            if (m.m == 0 && g.dh0)
+                store_row(g.dh0 + at, m, load_row(g.dh_last ? g.dh_last + at : nullptr, m));
             store_row(g.part + size_t(m.m) * g.B * g.C + at, m, float2{0.f, 0.f});
         }
         const int p0 = m.m * kTile + m.sub * kLen;
         pad<D>(g, g.dx, g.dx_sb, g.dx_sr, m, p0);
         pad<D>(g, g.dr, g.dr_sb, g.dr_sr, m, p0);
         pad<D>(g, g.di, g.di_sb, g.di_sr, m, p0);
-        return;
+    } else if (full_tile(g, m, m.valid - 1 - m.m)) {
+        tile_bwd<D, SPREAD, true>(g, m, rev, sh);
+    } else {
+        tile_bwd<D, SPREAD, false>(g, m, rev, sh);
     }
-    if (full_tile(g, m, m.valid - 1 - m.m)) tile_bwd<D, SPREAD, true>(g, m, rev, sh);
-    else tile_bwd<D, SPREAD, false>(g, m, rev, sh);
 }
 
 // 16 channels by 32 threads along the rows of partial sums; the threads' sums
@@ -470,8 +462,8 @@ __global__ __launch_bounds__(256) void k_step(int C, int S, const typename D::S*
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (!on || e >= n) continue;
-        float a, v;
-        gate_fwd(qx.get(e), qr.get(e), qi.get(e), decay * softplus(lam[c + e]) * kLog2e, a, v);
+        float a, v, sr, si;
+        gate_fwd(qx.get(e), qr.get(e), qi.get(e), rate_of(decay, lam[c + e]), a, v, sr, si);
         float* s = state + (long long)slot * C + c + e;
         out[e] = fmaf(a, *s, v);
         *s = out[e];
@@ -479,9 +471,13 @@ __global__ __launch_bounds__(256) void k_step(int C, int S, const typename D::S*
     put2<D>(h + b * hs + c, out[0], out[1], n);
 }
 
+unsigned units_of(const Args& a) {
+    return (a.C + kChan - 1) / kChan * unsigned(a.B) * unsigned(a.tiles);
+}
+
 template <class D>
 void launch(bool bwd, bool rev, const Args& a, hipStream_t st) {
-    const dim3 grid((a.C + kChan - 1) / kChan * unsigned(a.B) * unsigned(a.tiles));
+    const dim3 grid(units_of(a));
     if (a.tiles == 1) {
         if (bwd) k_tokens_bwd<D, false><<<grid, kThreads, 0, st>>>(a, rev);
         else k_tokens_fwd<D, false><<<grid, kThreads, 0, st>>>(a, rev);
@@ -532,7 +528,7 @@ hipError_t tokens_run(const gscan_shape& s, bool bwd, Args& a, void* ws, hipStre
     a.tiles = p.tiles;
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + words);
     if (words) {
-        a.carry = carry_at(ws, size_t(s.B) * s.C, p.tiles);
+        a.carry = carry_at(ws, size_t(s.B) * s.C, p.tiles, units_of(a), 1);
         const hipError_t e = clear_carry(ws, words, st);
         if (e != hipSuccess) return e;
     }

@@ -155,6 +155,25 @@ def test_long_sequences(layout):
     check(make(2, 3, 5000, "bf16", layout, 4), layout, reverse=True, lengths=[4999, 2100], what=(layout, 5000))
 
 
+@pytest.mark.parametrize("layout", ["bct", "btc"])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_spread_tiles(layout, reverse):
+    """Few rows: the tiles of a row lie in several workgroups (2048 positions of a plane, 128 of
+    tokens each), in groups of 16; lengths that end in any of them, or before the first."""
+    lengths = [4100, 0, 1, 2048, 2049, 4096, 127, 129, 2500]
+    d = make(len(lengths), 2, 4100, "f32", layout, 21)
+    for b, n in enumerate(lengths):
+        for k in ("x", "r", "i", "dh"):
+            t = d[k] if layout == "bct" else d[k].transpose(1, 2)
+            t[b, :, n:] = float("nan")
+    check(d, layout, lengths=lengths, reverse=reverse, what=(layout, reverse, 4100))
+
+
+@pytest.mark.parametrize("layout,T,dtype", [("bct", 35000, "f32"), ("btc", 2300, "f16")])
+def test_past_a_group_of_tiles(layout, T, dtype):
+    check(make(1, 3, T, dtype, layout, 22), layout, what=(layout, T, dtype))
+
+
 def test_planes_of_images():
     d = make(2, 3, 14 * 14, "f32", "bct", 5)
     import aware_conv_amd as A
