@@ -43,7 +43,8 @@ __device__ __forceinline__ unsigned take_share(const Carry& c, unsigned* shared)
     if (threadIdx.x == 0)
         *shared = c.share * __hip_atomic_fetch_add(c.next, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
-    return *shared;
+    // uniform, and known to be: what is derived from it stays scalar
+    return __builtin_amdgcn_readfirstlane(*shared);
 }
 
 __device__ __forceinline__ void publish_map(unsigned long long* p, float a, float h) {
