@@ -84,17 +84,28 @@ __device__ __forceinline__ float lane_sum(float v) {
 }
 
 // Positions p0 .. p0 + V - 1 of a row in scan order, `len` of them valid.
-// REV: position p lies at len - 1 - p.  FULL: all V are valid.
+// REV: position p lies at len - 1 - p.  FULL: all V are valid.  Where a row
+// ends within a lane's positions, the wavefront loads elements one by one, but
+// without a branch between the loads: those past the end read the last one,
+// which is not used.
 template <class D, int V, bool REV, bool FULL>
 __device__ __forceinline__ void fetch(Raw<D, V>& out, const typename D::S* row, int p0, int len) {
-    if (FULL || p0 + V <= len) {
+    if (FULL) {
         load_vec<D, V>(out, row + (REV ? len - V - p0 : p0));
-    } else {
+        return;
+    }
 #pragma unroll
-        for (int k = 0; k < Raw<D, V>::kWords; ++k) out.w[k] = 0;
+    for (int k = 0; k < Raw<D, V>::kWords; ++k) out.w[k] = 0;
+    if (!__any(p0 < len && len < p0 + V)) {
+        if (p0 + V <= len) load_vec<D, V>(out, row + (REV ? len - V - p0 : p0));
+    } else if (len > 0) {
+        float v[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (p0 + j < len) out.set(REV ? V - 1 - j : j, load_one<D>(row + (REV ? len - 1 - p0 - j : p0 + j)));
+        for (int j = 0; j < V; ++j) {
+            const int p = min(p0 + j, len - 1);
+            v[REV ? V - 1 - j : j] = load_one<D>(row + (REV ? len - 1 - p : p));
+        }
+        out = pack<D, false>(v);  // exact: the values are of the type
     }
 }
 // The same positions written; those in len .. T - 1 (which lie at their own
@@ -200,7 +211,8 @@ struct Bwd {
             A *= a[j];
         }
 #pragma unroll
-        for (int j = V - 1; j >= 0; --j) U = a[j] * (at<D, V, REV>(qd, j) + U);
+        for (int j = V - 1; j >= 0; --j)
+            U = FULL || p0 + j < w.len ? a[j] * (at<D, V, REV>(qd, j) + U) : 0.f;
     }
     // returns the lane's part of the sum for dlam
     __device__ __forceinline__ float close(const Args& g, const Row& w, int p0, float rate, float s,
@@ -214,10 +226,11 @@ struct Bwd {
         float ox[V], orr[V], oi[V], sum = 0.f;
 #pragma unroll
         for (int j = V - 1; j >= 0; --j) {
-            const float gt = at<D, V, REV>(qd, j) + u;
+            const bool in = FULL || p0 + j < w.len;
+            const float gt = (in ? at<D, V, REV>(qd, j) : 0.f) + u;
             float e;
             gate_bwd(at<D, V, REV>(qx, j), sr[j], si[j], rate, a[j], b[j], gt, ox[j], orr[j], oi[j], e);
-            sum += FULL || p0 + j < w.len ? e : 0.f;
+            sum += in ? e : 0.f;
             u = a[j] * gt;
         }
         put<D, V, REV, FULL>(row_of<S>(g.dx, g.dx_sb, g.dx_sr, w.b, w.c), ox, p0, w.len, g.T);
