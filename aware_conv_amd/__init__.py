@@ -21,21 +21,18 @@ __all__ = ["WTConv2d", "WTConvFunction", "wtconv_fwd", "wtconv_bwd_input",
            "adamw_grad_norm", "adamw_step", "AdamW"]
 
 
+_HOMES = {"_lib": ("wtconv_fwd", "wtconv_bwd_input", "wtconv_bwd_weight",
+                   "wtconv_workspace_size", "wtconv_strerror", "make_shape"),
+          "module": ("WTConv2d", "WTConvFunction", "GatedScan2d"),
+          "gscan": ("gscan_fwd", "gscan_bwd", "gscan_step", "gated_scan", "GatedScanFunction"),
+          "adamw": ("adamw_grad_norm", "adamw_step", "AdamW")}
+
+
 def __getattr__(name):
-    if name in ("wtconv_fwd", "wtconv_bwd_input", "wtconv_bwd_weight",
-                "wtconv_workspace_size", "wtconv_strerror", "make_shape"):
-        from . import _lib
-        return getattr(_lib, name)
-    if name in ("WTConv2d", "WTConvFunction"):
-        from . import module
-        return getattr(module, name)
-    if name in ("gscan_fwd", "gscan_bwd", "gscan_step", "gated_scan", "GatedScanFunction"):
-        from . import gscan
-        return getattr(gscan, name)
-    if name == "GatedScan2d":
-        from . import module
-        return module.GatedScan2d
-    if name in ("adamw_grad_norm", "adamw_step", "AdamW"):
-        from . import adamw
-        return getattr(adamw, name)
+    for home, names in _HOMES.items():
+        if name in names:
+            import importlib
+            value = getattr(importlib.import_module("." + home, __name__), name)
+            globals()[name] = value  # found directly from now on
+            return value
     raise AttributeError(name)

@@ -7,11 +7,13 @@ given as tensors, the learning rate and the gradient scale stay on the device:
 a step neither synchronises nor copies, and can be captured into a graph.
 """
 import ctypes
+import operator
 
 import numpy as np
 import torch
 
 from . import _lib
+from .gscan import _raw_stream
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 BLOCK = 256
@@ -24,20 +26,28 @@ def _dtype_code(dtype):
     return DTYPES[dtype]
 
 
+# Lists of tensors are checked attribute by attribute, with maps over the
+# attributes' own getters: a step over a hundred small tensors takes about as
+# long on the host as on the GPU, and this is most of it.
+_dtypes = operator.attrgetter("dtype")
+_numel, _contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
+_device, _address = torch.Tensor.get_device, torch.Tensor.data_ptr
+
+
 def _check_list(name, ts, count, dtype, device, numels):
     """Every tensor of the list: of `dtype`, on `device`, contiguous, of its number of elements."""
     if len(ts) != count:
         raise ValueError("%s holds %d tensors, expected %d" % (name, len(ts), count))
-    if not all(isinstance(t, torch.Tensor) for t in ts):
+    if not all(issubclass(c, torch.Tensor) for c in set(map(type, ts))):
         raise TypeError("%s must hold tensors" % name)
-    if any(t.dtype != dtype for t in ts):
+    if set(map(_dtypes, ts)) != {dtype}:
         raise TypeError("%s must hold %s tensors" % (name, dtype))
-    if any(t.device != device for t in ts):
+    if set(map(_device, ts)) != {device.index}:
         raise ValueError("%s must lie on %s" % (name, device))
-    if not all(t.is_contiguous() for t in ts):
+    if not all(map(_contiguous, ts)):
         raise ValueError("%s must be contiguous" % name)
-    if numels is not None and [t.numel() for t in ts] != numels:
-        raise ValueError("%s have sizes %s, expected %s" % (name, [t.numel() for t in ts], numels))
+    if numels is not None and list(map(_numel, ts)) != numels:
+        raise ValueError("%s have sizes %s, expected %s" % (name, list(map(_numel, ts)), numels))
 
 
 def _gpu_of(name, ts):
@@ -62,7 +72,7 @@ def _table(columns, numels):
     t = np.zeros((len(numels), 8), dtype=np.int64)
     for k, ts in enumerate(columns):
         if ts is not None:
-            t[:, k] = [x.data_ptr() for x in ts]
+            t[:, k] = np.fromiter(map(_address, ts), np.int64, len(ts))
     t[:, 7] = numels
     return t
 
@@ -91,11 +101,11 @@ def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, stream=Non
         norm = torch.empty(1, dtype=torch.float32, device=device)
     else:
         _scalar("norm", norm, device)
-    table = _table([None, grads], [t.numel() for t in grads])
+    table = _table([None, grads], list(map(_numel, grads)))
     ws, nws = _workspace(table, device, workspace)
     p = _lib._ptr
     _lib._check(_lib.lib.adamw_grad_norm(code, table.ctypes.data, len(table), scale, p(scale_dev),
-                                         p(norm), p(ws), nws, _lib._stream(stream, device)),
+                                         p(norm), p(ws), nws, _raw_stream(stream, device)),
                 "adamw_grad_norm")
     return norm
 
@@ -116,7 +126,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     device = _gpu_of("params", params)
     dtype, count = params[0].dtype, len(params)
     code = _dtype_code(dtype)
-    numels = [t.numel() for t in params]
+    numels = list(map(_numel, params))
     _check_list("params", params, count, dtype, device, None)
     _check_list("grads", grads, count, dtype, device, numels)
     state = CODES if scales is not None else torch.float32
@@ -130,6 +140,14 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
         blocks = [-(-n // BLOCK) for n in numels]
         _check_list("scales[0]", ms, count, torch.float32, device, blocks)
         _check_list("scales[1]", vs, count, torch.float32, device, blocks)
+    _step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas, eps, weight_decay, masters,
+          (ms, vs), numels, code, device, grad_scale, grad_norm, max_norm, workspace, stream)
+
+
+def _step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas, eps, weight_decay, masters,
+          scales, numels, code, device, grad_scale, grad_norm, max_norm, workspace=None, stream=None):
+    """The call, for lists that were checked or are the optimizer's own."""
+    ms, vs = scales
     if not isinstance(step, torch.Tensor) or step.dtype != torch.int32 or step.numel() != 1 or \
             step.device != device:
         raise ValueError("step must be one int32 on %s" % device)
@@ -144,11 +162,11 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     table = _table([params, grads, masters, exp_avgs, exp_avg_sqs, ms, vs], numels)
     ws, nws = _workspace(table, device, workspace)
     p = _lib._ptr
-    config = _lib.AdamwConfig(code, 8 if scales is not None else 32, lr, betas[0], betas[1], eps,
+    config = _lib.AdamwConfig(code, 8 if ms is not None else 32, lr, betas[0], betas[1], eps,
                               weight_decay, scale, max_norm or 0.0, p(lr_dev), p(scale_dev),
                               p(grad_norm))
-    _lib._check(_lib.lib.adamw_step(ctypes.byref(config), table.ctypes.data, count, p(step), p(ws),
-                                    nws, _lib._stream(stream, device)), "adamw_step")
+    _lib._check(_lib.lib.adamw_step(ctypes.byref(config), table.ctypes.data, len(numels), p(step), p(ws),
+                                    nws, _raw_stream(stream, device)), "adamw_step")
 
 
 class AdamW(torch.optim.Optimizer):
@@ -255,11 +273,12 @@ class AdamW(torch.optim.Optimizer):
             def column(name):
                 return [s[name] for s in st] if name in st[0] else None
 
-            scales = None
-            if self.bits == 8:
-                scales = column("exp_avg_scale"), column("exp_avg_sq_scale")
-            adamw_step(ps, gs, column("exp_avg"), column("exp_avg_sq"), step, lr=group["lr"],
-                       betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
-                       masters=column("master"), scales=scales, grad_scale=self.grad_scale,
-                       grad_norm=norm, max_norm=self.max_norm)
+            device, dtype, count = _gpu_of("parameters", ps), ps[0].dtype, len(ps)
+            numels = list(map(_numel, ps))
+            _check_list("parameters", ps, count, dtype, device, None)
+            _check_list("gradients", gs, count, dtype, device, numels)
+            scales = column("exp_avg_scale"), column("exp_avg_sq_scale")
+            _step(ps, gs, column("exp_avg"), column("exp_avg_sq"), step, group["lr"],
+                  group["betas"], group["eps"], group["weight_decay"], column("master"), scales,
+                  numels, _dtype_code(dtype), device, self.grad_scale, norm, self.max_norm)
         return loss

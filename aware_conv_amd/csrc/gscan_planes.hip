@@ -322,11 +322,13 @@ __global__ __launch_bounds__(kThreads) void k_planes_bwd(Args g) {
 // the tiles of a row spread over workgroups
 // ---------------------------------------------------------------------------
 
-constexpr int kWaves = kThreads / 64;
+constexpr int kSpread = 512;  // threads of a tile
+constexpr int kWaves = kSpread / 64;
 constexpr int kWideV = 8;
-constexpr int kWide = kThreads * kWideV;  // positions of a tile
-// Units of a share: 8x64x512x512 fp32 forward 799 us one by one (the counter's
-// pace), 467 us with 8.
+constexpr int kWide = kSpread * kWideV;  // positions of a tile
+// Units of a share at the most: 8x64x512x512 fp32 forward 799 us with tiles of
+// 2048 positions taken one by one (the counter's pace), 467 with shares of 8
+// of them, 443 with shares of 8 tiles of 4096.
 constexpr unsigned kShare = 8;
 
 struct Spread {
@@ -397,13 +399,13 @@ template <class D>
 __device__ __forceinline__ void pad(const Args& g, const Unit& u, void* out, long long sb, long long sr) {
     using S = typename D::S;
     S* row = row_of<S>(out, sb, sr, u.w.b, u.w.c);
-    for (int p = u.m * kWide + threadIdx.x; p < min(g.T, (u.m + 1) * kWide); p += kThreads)
+    for (int p = u.m * kWide + threadIdx.x; p < min(g.T, (u.m + 1) * kWide); p += kSpread)
         store_one<D>(row + p, 0.f);
 }
 
 template <class D, bool REV, bool FULL>
 __device__ __forceinline__ void spread_fwd(const Args& g, const Unit& u, Spread& sh) {
-    const int wave = threadIdx.x / 64, p0 = (u.m * kThreads + threadIdx.x) * kWideV;
+    const int wave = threadIdx.x / 64, p0 = (u.m * kSpread + threadIdx.x) * kWideV;
     Fwd<D, kWideV, REV, FULL> t;
     t.open(g, u.w, p0, rate_of(g.decay, g.lam[u.w.c]));
     lane_scan<64>(t.A, t.H);
@@ -412,7 +414,7 @@ __device__ __forceinline__ void spread_fwd(const Args& g, const Unit& u, Spread&
         sh.H[wave] = t.H;
     }
     __syncthreads();
-    if (threadIdx.x == kThreads - 1) {
+    if (threadIdx.x == kSpread - 1) {
         float a = sh.A[0], h = sh.H[0];
         for (int k = 1; k < kWaves; ++k) {
             h = fmaf(sh.A[k], h, sh.H[k]);
@@ -430,13 +432,13 @@ __device__ __forceinline__ void spread_fwd(const Args& g, const Unit& u, Spread&
     __syncthreads();
     float s = sh.carry;
     for (int k = 0; k < wave; ++k) s = fmaf(sh.A[k], s, sh.H[k]);
-    if (threadIdx.x == kThreads - 1) give_state(g, u, g.h_last, fmaf(t.A, s, t.H));
+    if (threadIdx.x == kSpread - 1) give_state(g, u, g.h_last, fmaf(t.A, s, t.H));
     s = fmaf(lane_before<64>(t.A, 1.f), s, lane_before<64>(t.H, 0.f));
     t.close(g, u.w, p0, s);
 }
 
 template <class D, bool REV>
-__global__ __launch_bounds__(kThreads) void k_spread_fwd(Args g) {
+__global__ __launch_bounds__(kSpread) void k_spread_fwd(Args g) {
     __shared__ Spread sh;
     const unsigned from = take_share(g.carry, &sh.unit);
     for (unsigned k = from; k < min(from + g.carry.share, g.carry.units); ++k) {
@@ -456,7 +458,7 @@ __global__ __launch_bounds__(kThreads) void k_spread_fwd(Args g) {
 template <class D, bool REV, bool FULL>
 __device__ __forceinline__ void spread_bwd(const Args& g, const Unit& u, Spread& sh) {
     const int wave = threadIdx.x / 64, n = u.valid - 1 - u.m;
-    const int p0 = (n * kThreads + threadIdx.x) * kWideV;
+    const int p0 = (n * kSpread + threadIdx.x) * kWideV;
     const long long rows = (long long)g.B * g.C;
     const float rate = rate_of(g.decay, g.lam[u.w.c]);
     float s = g.states[n * rows + u.w.id];
@@ -471,7 +473,7 @@ __device__ __forceinline__ void spread_bwd(const Args& g, const Unit& u, Spread&
         sh.U[wave] = U;
     }
     __syncthreads();
-    if (threadIdx.x == kThreads - 1) {
+    if (threadIdx.x == kSpread - 1) {
         float a = sh.A[kWaves - 1], h = sh.U[kWaves - 1];
         for (int k = kWaves - 2; k >= 0; --k) {
             h = fmaf(sh.A[k], h, sh.U[k]);
@@ -502,7 +504,7 @@ __device__ __forceinline__ void spread_bwd(const Args& g, const Unit& u, Spread&
 }
 
 template <class D, bool REV>
-__global__ __launch_bounds__(kThreads) void k_spread_bwd(Args g) {
+__global__ __launch_bounds__(kSpread) void k_spread_bwd(Args g) {
     __shared__ Spread sh;
     const unsigned from = take_share(g.carry, &sh.unit);
     for (unsigned k = from; k < min(from + g.carry.share, g.carry.units); ++k) {
@@ -532,7 +534,17 @@ __global__ __launch_bounds__(kThreads) void k_spread_bwd(Args g) {
 // workgroups.  By the shape alone, so that the states of a forward call fit
 // the backward one: the narrowest group that holds the row in one tile, else
 // whole wavefronts of 8 positions per lane.
-constexpr long long kFewRows = 4096;
+//
+// A wavefront that walks a row takes about 0.85 us per tile of 512, whatever
+// else runs; spreading costs about 15 us and the counter's 13 ns per tile of
+// 4096.  Forward + backward, walked and spread, fp32: 16 rows of 12544
+// positions 62 and 42 us, 256 of 12544 71 and 56, 256 of 50176 297 and 149,
+// 768 of 12544 96 and 125, 768 of 50176 398 and 385, 1536 of 50176 763 and 728
+// (bf16 there 410 and 460).
+bool spread(const gscan_shape& s) {
+    const long long rows = (long long)s.B * s.C;
+    return rows <= 1024 && s.T > 32 * (rows < 256 ? 256 : rows);
+}
 struct Form {
     int V, LW;
 };
@@ -540,7 +552,7 @@ Form form_of(const gscan_shape& s) {
     if (s.T <= 4) return {4, 1};
     if (s.T <= 64) return {4, 16};
     if (s.T <= 256) return {4, 64};
-    if (s.T > kWide && (long long)s.B * s.C < kFewRows) return {kWideV, 0};
+    if (spread(s)) return {kWideV, 0};
     return {8, 64};
 }
 
@@ -561,11 +573,11 @@ template <class D>
 void launch_spread(bool bwd, bool rev, const Args& a, hipStream_t st) {
     const dim3 grid(shares(a.carry));
     if (bwd) {
-        if (rev) k_spread_bwd<D, true><<<grid, kThreads, 0, st>>>(a);
-        else k_spread_bwd<D, false><<<grid, kThreads, 0, st>>>(a);
+        if (rev) k_spread_bwd<D, true><<<grid, kSpread, 0, st>>>(a);
+        else k_spread_bwd<D, false><<<grid, kSpread, 0, st>>>(a);
     } else {
-        if (rev) k_spread_fwd<D, true><<<grid, kThreads, 0, st>>>(a);
-        else k_spread_fwd<D, false><<<grid, kThreads, 0, st>>>(a);
+        if (rev) k_spread_fwd<D, true><<<grid, kSpread, 0, st>>>(a);
+        else k_spread_fwd<D, false><<<grid, kSpread, 0, st>>>(a);
     }
 }
 template <class D>

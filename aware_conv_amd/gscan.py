@@ -7,6 +7,7 @@ or bfloat16.  Elements along the last axis are adjacent; the other strides are
 free, so that x and the gates may be chunks of one projection.
 """
 import ctypes
+import functools
 
 import torch
 
@@ -41,74 +42,105 @@ def _rows_and_run(shape, layout):
 
 def _adjacent(t):
     """Whether a row of `t` (its last axis, or the planes of a 4-D tensor) is one run."""
-    n = t.dim()
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return True
-    if n == 4:
-        return ((t.shape[3] == 1 or t.stride(3) == 1) and
-                (t.shape[2] == 1 or t.stride(2) == t.shape[3]))
-    return t.shape[-1] == 1 or t.stride(-1) == 1
+    shape, st = t.shape, t.stride()
+    if len(shape) == 4 and not (shape[2] == 1 or st[2] == shape[3]):
+        return False
+    return shape[-1] == 1 or st[-1] == 1
 
 
-def _view(t):
+# The checks below and the marshalling run once per call and tensor; small calls
+# take about as long as they do, so each is one function per tensor that asks
+# for every attribute once, and pointers go to ctypes as plain integers.
+
+def _act(name, t, shape, dtype, device):
+    """The view of an activation that is `shape`, `dtype`, on `device` and has adjacent rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if not _adjacent(t):
+        raise ValueError("%s must have adjacent elements along its rows" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s; every tensor must be on %s" % (name, t.device, device))
+    st = t.stride()
+    return ctypes.byref(_View(t.data_ptr(), st[0], st[1]))
+
+
+def _flat(name, t, shape, dtype, device):
+    """The address of a contiguous tensor of `shape` and `dtype` on `device`; None for None."""
     if t is None:
         return None
-    return ctypes.byref(_lib.GscanView(t.data_ptr() or None, t.stride(0), t.stride(1)))
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s; every tensor must be on %s" % (name, t.device, device))
+    return t.data_ptr()
 
 
-def _expect_acts(x, acts):
-    for name, t in acts:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % name)
-        if t.shape != x.shape:
-            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(x.shape)))
-        if t.dtype != x.dtype:
-            raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, x.dtype))
-        if not _adjacent(t):
-            raise ValueError("%s must have adjacent elements along its rows" % name)
+_View = _lib.GscanView
+_f32, _i32 = torch.float32, torch.int32
 
 
-def _call(x, acts, flats, layout, reverse, decay, workspace):
-    """Checks shared by fwd and bwd; `flats`: (name, tensor, shape, dtype).  Returns the shape
-    struct."""
+def _input(x):
+    """(dtype code, dtype, device) of the tensor that the others go by."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
+    return _dtype_code(x), x.dtype, x.device
+
+
+def _on_gpu(device):
+    if device.type != "cuda":
+        raise ValueError("x is on %s; every tensor must be on a GPU" % device)
+
+
+def _raw_stream(stream, device):
+    """The stream's handle; without a stream, that of the current one, as an integer (a Stream
+    object would cost as much as the rest of a small call's marshalling)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@functools.lru_cache(maxsize=256)
+def _sizes(B, C, T, layout, code):
+    """(floats of the states, bytes of the workspace) for a shape."""
+    s = _lib.GscanShape(B, C, T, layout, code, 0, 1.0)
+    out = []
+    for fn in ("gscan_states_size", "gscan_workspace_size"):
+        n = ctypes.c_size_t(0)
+        _lib._check(getattr(_lib.lib, fn)(ctypes.byref(s), ctypes.byref(n)), fn)
+        out.append(n.value)
+    return out[0] // 4, out[1]
+
+
+def _shape(x, code, layout, reverse, decay):
     B, C, T = _rows_and_run(x.shape, layout)
     if T > MAX_T:
         raise ValueError("at most %d positions are supported, got %d" % (MAX_T, T))
-    code = _dtype_code(x)
-    _expect_acts(x, acts)
-    for name, t, shape, dtype in flats:
-        _lib._expect(dtype, [(name, t, shape(B, C))])
-    _lib._expect(None, [("workspace", workspace, None)])
-    _lib._on_gpu(x, list(acts) + [(n, t) for n, t, _, _ in flats] + [("workspace", workspace)])
-    return _lib.GscanShape(B, C, T, LAYOUTS[layout], code, int(bool(reverse)), decay)
-
-
-def _size(fn, s):
-    n = ctypes.c_size_t(0)
-    _lib._check(getattr(_lib.lib, fn)(ctypes.byref(s), ctypes.byref(n)), fn)
-    return n.value
+    return _lib.GscanShape(B, C, T, LAYOUTS[layout], code, 1 if reverse else 0, decay)
 
 
 def _workspace(s, device, workspace):
+    """(tensor, address, bytes); the caller keeps the tensor until the call was enqueued."""
     if workspace is None:
-        need = _size("gscan_workspace_size", s)
+        need = _sizes(s.B, s.C, s.T, s.layout, s.dtype)[1]
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return workspace, workspace.numel() * workspace.element_size()
-
-
-def _per_row(B, C):
-    return (B, C)
+    p = _flat("workspace", workspace, None, None, device)
+    return workspace, p, workspace.numel() * workspace.element_size()
 
 
 def gscan_workspace_size(x, layout="bct"):
     """Bytes of workspace gscan_fwd and gscan_bwd need for activations like x."""
     B, C, T = _rows_and_run(x.shape, layout)
-    return _size("gscan_workspace_size",
-                 _lib.GscanShape(B, C, T, LAYOUTS[layout], _dtype_code(x), 0, 1.0))
+    return _sizes(B, C, T, LAYOUTS[layout], _dtype_code(x))[1]
 
 
 def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, decay=8.0, h=None,
@@ -116,22 +148,27 @@ def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, 
     """(h, h_last, states) of the recurrence: h like x, h_last [B, C] fp32 the state after the
     last valid position, states what gscan_bwd needs (None unless ``save_states``).  lam [C] and
     h0 [B, C] are fp32, lengths [B] int32 (see include/gscan.h)."""
-    s = _call(x, [("x", x), ("r", r), ("i", i), ("h", h)],
-              [("lam", lam, lambda B, C: (C,), torch.float32), ("h0", h0, _per_row, torch.float32),
-               ("lengths", lengths, lambda B, C: (B,), torch.int32)],
-              layout, reverse, decay, workspace)
-    dev = x.device
+    code, dt, dev = _input(x)
+    s = _shape(x, code, layout, reverse, decay)
+    shape, rows = x.shape, (s.B, s.C)
+    px, pr, pi = _act("x", x, shape, dt, dev), _act("r", r, shape, dt, dev), _act("i", i, shape, dt, dev)
+    plam = _flat("lam", lam, (s.C,), _f32, dev)
+    ph0 = _flat("h0", h0, rows, _f32, dev)
+    plen = _flat("lengths", lengths, (s.B,), _i32, dev)
+    if h is not None:
+        _act("h", h, shape, dt, dev)
+    _on_gpu(dev)
     if h is None:
-        h = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    h_last = torch.empty((s.B, s.C), dtype=torch.float32, device=dev)
-    states = None
+        h = torch.empty(shape, dtype=dt, device=dev)
+    h_last = torch.empty(rows, dtype=_f32, device=dev)
+    states = pstates = None
     if save_states:
-        states = torch.empty(_size("gscan_states_size", s) // 4, dtype=torch.float32, device=dev)
-    ws, nws = _workspace(s, dev, workspace)
-    p = _lib._ptr
-    _lib._check(_lib.lib.gscan_fwd(ctypes.byref(s), _view(x), _view(r), _view(i), p(lam), p(h0),
-                                   p(lengths), _view(h), p(h_last), p(states), p(ws), nws,
-                                   _lib._stream(stream, dev)), "gscan_fwd")
+        states = torch.empty(_sizes(s.B, s.C, s.T, s.layout, code)[0], dtype=_f32, device=dev)
+        pstates = states.data_ptr()
+    ws, pws, nws = _workspace(s, dev, workspace)
+    _lib._check(_lib.lib.gscan_fwd(ctypes.byref(s), px, pr, pi, plam, ph0, plen,
+                                   _act("h", h, shape, dt, dev), h_last.data_ptr(), pstates, pws, nws,
+                                   _raw_stream(stream, dev)), "gscan_fwd")
     return h, h_last, states
 
 
@@ -144,32 +181,34 @@ def gscan_bwd(x, r, i, lam, states, dh, dh_last=None, lengths=None, layout="bct"
     unknown = [n for n in grads if n not in GRAD_NAMES]
     if unknown:
         raise KeyError("unknown gradients %s" % ", ".join(map(str, unknown)))
-    acts = [("x", x), ("r", r), ("i", i), ("dh", dh)]
-    acts += [("grads[%s]" % n, grads.get(n)) for n in ("dx", "dr", "di")]
-    flats = [("lam", lam, lambda B, C: (C,), torch.float32),
-             ("dh_last", dh_last, _per_row, torch.float32),
-             ("lengths", lengths, lambda B, C: (B,), torch.int32),
-             ("grads[dlam]", grads.get("dlam"), lambda B, C: (C,), torch.float32),
-             ("grads[dh0]", grads.get("dh0"), _per_row, torch.float32)]
-    s = _call(x, acts, flats, layout, reverse, decay, workspace)
+    code, dt, dev = _input(x)
+    s = _shape(x, code, layout, reverse, decay)
+    shape, rows = x.shape, (s.B, s.C)
+    px, pr, pi = _act("x", x, shape, dt, dev), _act("r", r, shape, dt, dev), _act("i", i, shape, dt, dev)
+    pdh = _act("dh", dh, shape, dt, dev)
+    plam = _flat("lam", lam, (s.C,), _f32, dev)
+    plast = _flat("dh_last", dh_last, rows, _f32, dev)
+    plen = _flat("lengths", lengths, (s.B,), _i32, dev)
+    for n in ("dx", "dr", "di"):
+        if grads.get(n) is not None:
+            _act("grads[%s]" % n, grads[n], shape, dt, dev)
+    for n, sh in (("dlam", (s.C,)), ("dh0", rows)):
+        _flat("grads[%s]" % n, grads.get(n), sh, _f32, dev)
     if states is None:
         raise ValueError("gscan_bwd needs the states of gscan_fwd(..., save_states=True)")
-    _lib._expect(torch.float32, [("states", states, (_size("gscan_states_size", s) // 4,))])
-    _lib._on_gpu(x, [("states", states)])
-    dev = x.device
+    pst = _flat("states", states, (_sizes(s.B, s.C, s.T, s.layout, code)[0],), _f32, dev)
+    _on_gpu(dev)
     for n in ("dx", "dr", "di"):
         if grads.get(n) is None:
-            grads[n] = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    for n, shape in (("dlam", (s.C,)), ("dh0", (s.B, s.C))):
+            grads[n] = torch.empty(shape, dtype=dt, device=dev)
+    for n, sh in (("dlam", (s.C,)), ("dh0", rows)):
         if grads.get(n) is None:
-            grads[n] = torch.empty(shape, dtype=torch.float32, device=dev)
-    ws, nws = _workspace(s, dev, workspace)
-    p = _lib._ptr
-    _lib._check(_lib.lib.gscan_bwd(ctypes.byref(s), _view(x), _view(r), _view(i), p(lam), p(states),
-                                   p(lengths), _view(dh), p(dh_last),
-                                   *[_view(grads[n]) for n in ("dx", "dr", "di")],
-                                   p(grads["dlam"]), p(grads["dh0"]), p(ws), nws,
-                                   _lib._stream(stream, dev)), "gscan_bwd")
+            grads[n] = torch.empty(sh, dtype=_f32, device=dev)
+    ws, pws, nws = _workspace(s, dev, workspace)
+    _lib._check(_lib.lib.gscan_bwd(ctypes.byref(s), px, pr, pi, plam, pst, plen, pdh, plast,
+                                   *[_act(n, grads[n], shape, dt, dev) for n in ("dx", "dr", "di")],
+                                   grads["dlam"].data_ptr(), grads["dh0"].data_ptr(), pws, nws,
+                                   _raw_stream(stream, dev)), "gscan_bwd")
     return grads
 
 
@@ -177,30 +216,26 @@ def gscan_step(x, r, i, lam, state, slots=None, decay=8.0, h=None, stream=None):
     """One position of B sequences: x, r, i [B, C] (free row strides), their states in rows
     ``slots`` (int32 [B]; the first B rows if None) of ``state`` [S, C] fp32, which is updated.
     Returns h [B, C].  Sequences whose slot is outside 0..S-1 give zeros and change nothing."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    if x.dim() != 2:
-        raise ValueError("activations must be [B, C], got shape %s" % (tuple(x.shape),))
-    B, C = x.shape
-    code = _dtype_code(x)
-    acts = [("x", x), ("r", r), ("i", i), ("h", h)]
-    _expect_acts(x, acts)
-    if not isinstance(state, torch.Tensor):
-        raise TypeError("state must be a torch.Tensor")
+    code, dt, dev = _input(x)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("activations must be [B, C], got shape %s" % (tuple(shape),))
+    B, C = shape
+    px, pr, pi = _act("x", x, shape, dt, dev), _act("r", r, shape, dt, dev), _act("i", i, shape, dt, dev)
+    plam = _flat("lam", lam, (C,), _f32, dev)
+    pstate = _flat("state", state, None, _f32, dev)
     if state.dim() != 2 or state.shape[1] != C:
         raise ValueError("state must be [S, %d], got shape %s" % (C, tuple(state.shape)))
-    flats = [("lam", lam, (C,)), ("state", state, None)]
-    _lib._expect(torch.float32, flats)
-    _lib._expect(torch.int32, [("slots", slots, (B,))])
-    if slots is None and state.shape[0] < B:
-        raise ValueError("state has %d rows for %d sequences" % (state.shape[0], B))
-    _lib._on_gpu(x, acts + [("lam", lam), ("state", state), ("slots", slots)])
+    S = state.shape[0]
+    pslots = _flat("slots", slots, (B,), _i32, dev)
+    if slots is None and S < B:
+        raise ValueError("state has %d rows for %d sequences" % (S, B))
+    _on_gpu(dev)
     if h is None:
-        h = torch.empty((B, C), dtype=x.dtype, device=x.device)
-    p = _lib._ptr
-    _lib._check(_lib.lib.gscan_step(B, C, state.shape[0], code, decay, _view(x), _view(r), _view(i),
-                                    p(lam), p(state), p(slots), _view(h),
-                                    _lib._stream(stream, x.device)), "gscan_step")
+        h = torch.empty(shape, dtype=dt, device=dev)
+    _lib._check(_lib.lib.gscan_step(B, C, S, code, decay, px, pr, pi, plam, pstate, pslots,
+                                    _act("h", h, shape, dt, dev), _raw_stream(stream, dev)),
+                "gscan_step")
     return h
 
 

@@ -158,18 +158,18 @@ def test_long_sequences(layout):
 @pytest.mark.parametrize("layout", ["bct", "btc"])
 @pytest.mark.parametrize("reverse", [False, True])
 def test_spread_tiles(layout, reverse):
-    """Few rows: the tiles of a row lie in several workgroups (2048 positions of a plane, 128 of
-    tokens each), in groups of 16; lengths that end in any of them, or before the first."""
-    lengths = [4100, 0, 1, 2048, 2049, 4096, 127, 129, 2500]
-    d = make(len(lengths), 2, 4100, "f32", layout, 21)
+    """Few rows: the tiles of a row lie in several workgroups (4096 positions of a plane, 128 or
+    256 of tokens each), in groups of 16; lengths that end in any of them, or before the first."""
+    lengths = [9000, 0, 1, 4096, 4097, 8192, 127, 129, 2500]
+    d = make(len(lengths), 2, 9000, "f32", layout, 21)
     for b, n in enumerate(lengths):
         for k in ("x", "r", "i", "dh"):
             t = d[k] if layout == "bct" else d[k].transpose(1, 2)
             t[b, :, n:] = float("nan")
-    check(d, layout, lengths=lengths, reverse=reverse, what=(layout, reverse, 4100))
+    check(d, layout, lengths=lengths, reverse=reverse, what=(layout, reverse, 9000))
 
 
-@pytest.mark.parametrize("layout,T,dtype", [("bct", 35000, "f32"), ("btc", 2300, "f16")])
+@pytest.mark.parametrize("layout,T,dtype", [("bct", 70000, "f32"), ("btc", 4400, "f16")])
 def test_past_a_group_of_tiles(layout, T, dtype):
     check(make(1, 3, T, dtype, layout, 22), layout, what=(layout, T, dtype))
 
