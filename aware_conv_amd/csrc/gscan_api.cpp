@@ -16,6 +16,10 @@ constexpr long long kMaxRows = 1LL << 25;
 size_t elem_size(int dtype) { return dtype == GSCAN_F32 ? 4 : 2; }
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+gsc::Plan plan_of(const gscan_shape& s) {
+    return s.layout == GSCAN_BCT ? gsc::planes_plan(s) : gsc::tokens_plan(s);
+}
+
 int check_shape(const gscan_shape* s) {
     if (!s) return WTCONV_ERR_NULL;
     if (s->B < 0 || s->C < 0 || s->T < 0 || s->T > (1 << 30)) return WTCONV_ERR_SHAPE;
@@ -24,11 +28,7 @@ int check_shape(const gscan_shape* s) {
     if (s->layout != GSCAN_BCT && s->layout != GSCAN_BTC) return WTCONV_ERR_LAYOUT;
     if (!(s->decay > 0.f) || !isfinite(s->decay)) return WTCONV_ERR_VALUE;
     if ((long long)s->B * s->C > kMaxRows) return WTCONV_ERR_SHAPE;
-    return WTCONV_OK;
-}
-
-gsc::Plan plan_of(const gscan_shape& s) {
-    return s.layout == GSCAN_BCT ? gsc::planes_plan(s) : gsc::tokens_plan(s);
+    return plan_of(*s).fits ? WTCONV_OK : WTCONV_ERR_UNSUPPORTED;
 }
 
 // A buffer of the call: `rows` runs of `run` adjacent elements per sequence.

@@ -30,9 +30,10 @@ struct Args {
 
 struct Plan {
     int tiles;       // tiles along time (at least 1); the states are [tiles][B][C]
-    int parts;       // rows of partial sums of dlam
+    long long parts;  // rows of partial sums of dlam
     size_t states;   // bytes
     size_t scratch;  // bytes of workspace
+    bool fits;       // one launch holds the call's threads (fewer than 2^32)
 };
 
 Plan planes_plan(const gscan_shape& s);
@@ -44,7 +45,7 @@ hipError_t tokens_fwd(const gscan_shape& s, Args a, void* ws, hipStream_t st);
 hipError_t tokens_bwd(const gscan_shape& s, Args a, void* ws, hipStream_t st);
 
 // dlam from `parts` rows of partial sums, added in order in fp64.
-hipError_t close_dlam(const Args& a, int parts, hipStream_t st);
+hipError_t close_dlam(const Args& a, long long parts, hipStream_t st);
 
 hipError_t step(int B, int C, int S, int dtype, float decay, const gscan_view& x,
                 const gscan_view& r, const gscan_view& i, const float* lam, float* state,

@@ -619,9 +619,10 @@ Plan planes_plan(const gscan_shape& s) {
     const int tile = f.LW == 0 ? kWide : f.V * f.LW;
     Plan p;
     p.tiles = s.T > 0 ? (s.T - 1) / tile + 1 : 1;
-    p.parts = f.LW == 0 ? p.tiles * s.B : s.B;
+    p.parts = f.LW == 0 ? (long long)p.tiles * s.B : s.B;
     p.states = sizeof(float) * size_t(p.tiles) * s.B * s.C;
     p.scratch = words_of(s, f, p.tiles) + sizeof(float) * size_t(p.parts) * s.C;
+    p.fits = f.LW != 0 || (double)s.B * s.C * p.tiles * kSpread < 4e9;
     return p;
 }
 

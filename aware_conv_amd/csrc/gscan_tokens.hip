@@ -451,13 +451,13 @@ __global__ __launch_bounds__(kLanes* kBwdSub, 2) void k_tokens_bwd(Args g, bool 
 // 16 channels by 32 threads along the rows of partial sums; the threads' sums
 // are added in order.
 constexpr int kCloseChan = 16, kCloseRows = 32;
-__global__ __launch_bounds__(kCloseChan* kCloseRows) void k_close_dlam(Args g, int parts) {
+__global__ __launch_bounds__(kCloseChan* kCloseRows) void k_close_dlam(Args g, long long parts) {
     __shared__ double acc[kCloseRows][kCloseChan];
     const int cl = threadIdx.x % kCloseChan, k = threadIdx.x / kCloseChan;
     const int c = blockIdx.x * kCloseChan + cl;
     double t = 0;
     if (c < g.C)
-        for (int p = k; p < parts; p += kCloseRows) t += double(g.part[size_t(p) * g.C + c]);
+        for (long long p = k; p < parts; p += kCloseRows) t += double(g.part[size_t(p) * g.C + c]);
     acc[k][cl] = t;
     __syncthreads();
     if (k == 0 && c < g.C) {
@@ -552,9 +552,10 @@ hipError_t clear_carry(void* ws, size_t bytes, hipStream_t st) {
 Plan tokens_plan(const gscan_shape& s) {
     Plan p;
     p.tiles = tiles_of(s.T, kStateTile);  // of the backward pass, the shorter ones
-    p.parts = p.tiles * s.B;
+    p.parts = (long long)p.tiles * s.B;
     p.states = sizeof(float) * size_t(p.tiles) * s.B * s.C;
     p.scratch = tokens_carry(s, p.tiles) + sizeof(float) * size_t(p.parts) * s.C;
+    p.fits = (double)((s.C + kChan - 1) / kChan) * s.B * p.tiles * kLanes * kFwdSub < 4e9;
     return p;
 }
 
@@ -585,7 +586,7 @@ hipError_t tokens_bwd(const gscan_shape& s, Args a, void* ws, hipStream_t st) {
     return e == hipSuccess ? close_dlam(a, tokens_plan(s).parts, st) : e;
 }
 
-hipError_t close_dlam(const Args& a, int parts, hipStream_t st) {
+hipError_t close_dlam(const Args& a, long long parts, hipStream_t st) {
     k_close_dlam<<<dim3((a.C + kCloseChan - 1) / kCloseChan), kCloseChan * kCloseRows, 0, st>>>(
         a, parts);
     return hipGetLastError();

@@ -77,6 +77,13 @@ typedef struct {
     long long sb, sr; /* strides of the batch and of a row, in elements, >= 0 */
 } gscan_view;
 
+/*
+ * Sizes: T up to 2^30, B * C up to 2^25 (WTCONV_ERR_SHAPE beyond).  Tokens of
+ * fewer than 64 channels, or planes, of so many positions that one launch does
+ * not hold their threads (2^31 positions or more in all) are refused with
+ * WTCONV_ERR_UNSUPPORTED.
+ */
+
 /* Bytes of the states gscan_fwd writes for gscan_bwd (what h held before each
  * of the tiles the kernels walk in). */
 int gscan_states_size(const gscan_shape* s, size_t* bytes);

@@ -65,6 +65,14 @@ def test_shapes(call, kw, code):
     assert call(shape(**kw)) == code
 
 
+@pytest.mark.parametrize("call", [fwd, bwd])
+def test_launches_that_would_not_fit(call):
+    assert call(shape(B=1 << 12, C=1, T=1 << 22, layout=1)) == -8
+    assert call(shape(B=1 << 4, C=1 << 6, T=1 << 30)) == -8
+    # the same tokens in whole tiles of channels
+    assert call(shape(B=1 << 6, C=64, T=1 << 22, layout=1), ws=None) in (ALIAS, SHAPE, WORKSPACE)
+
+
 def test_forward_arguments():
     assert fwd() == WORKSPACE  # everything before it is in order
     for n in ("x", "r", "i", "lam", "h"):
