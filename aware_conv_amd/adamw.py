@@ -7,13 +7,18 @@ given as tensors, the learning rate and the gradient scale stay on the device:
 a step neither synchronises nor copies, and can be captured into a graph.
 """
 import ctypes
-import operator
 
 import numpy as np
 import torch
 
 from . import _lib
 from .gscan import _raw_stream
+
+try:
+    from . import _lists
+except ImportError as e:
+    raise ImportError("_lists.so is not built (%s); run `python -m aware_conv_amd.build` or "
+                      "__graft_entry__.build() first" % e)
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 BLOCK = 256
@@ -26,28 +31,35 @@ def _dtype_code(dtype):
     return DTYPES[dtype]
 
 
-# Lists of tensors are checked attribute by attribute, with maps over the
-# attributes' own getters: a step over a hundred small tensors takes about as
-# long on the host as on the GPU, and this is most of it.
-_dtypes = operator.attrgetter("dtype")
-_numel, _contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
-_device, _address = torch.Tensor.get_device, torch.Tensor.data_ptr
+# Lists of tensors are checked, and their addresses written into the call's
+# table, by a small extension (pyext/tensor_lists.cpp).
+_PARAM, _GRAD, _MASTER, _M, _V, _M_SCALE, _V_SCALE, _COUNT = range(8)  # columns of the table
 
 
-def _check_list(name, ts, count, dtype, device, numels):
-    """Every tensor of the list: of `dtype`, on `device`, contiguous, of its number of elements."""
-    if len(ts) != count:
-        raise ValueError("%s holds %d tensors, expected %d" % (name, len(ts), count))
-    if not all(issubclass(c, torch.Tensor) for c in set(map(type, ts))):
-        raise TypeError("%s must hold tensors" % name)
-    if set(map(_dtypes, ts)) != {dtype}:
-        raise TypeError("%s must hold %s tensors" % (name, dtype))
-    if set(map(_device, ts)) != {device.index}:
-        raise ValueError("%s must lie on %s" % (name, device))
-    if not all(map(_contiguous, ts)):
-        raise ValueError("%s must be contiguous" % name)
-    if numels is not None and list(map(_numel, ts)) != numels:
-        raise ValueError("%s have sizes %s, expected %s" % (name, list(map(_numel, ts)), numels))
+def _column(table, column, name, ts, dtype, device, block=1):
+    """The list's addresses into the table, after checking that its tensors are of `dtype`, on
+    `device`, contiguous, and of ceil(n / block) elements for the n of the table's last column
+    (block 0: of any number, which that column then takes)."""
+    code, k = _lists.column(ts, table.ctypes.data, len(table), column, dtype, device.index, block)
+    if code == 0:
+        return
+    if code == 1:
+        raise ValueError("%s holds %d tensors, expected %d" % (name, len(ts), len(table)))
+    if code == 2:
+        raise TypeError("%s[%d] must be a torch.Tensor" % (name, k))
+    t = ts[k]
+    if code == 3:
+        raise TypeError("%s[%d] has dtype %s, expected %s" % (name, k, t.dtype, dtype))
+    if code == 4:
+        raise ValueError("%s[%d] is on %s, expected %s" % (name, k, t.device, device))
+    if code == 5:
+        raise ValueError("%s[%d] must be contiguous" % (name, k))
+    raise ValueError("%s[%d] has %d elements, expected %d"
+                     % (name, k, t.numel(), -(-int(table[k, _COUNT]) // block)))
+
+
+def _new_table(count):
+    return np.zeros((count, 8), dtype=np.int64)
 
 
 def _gpu_of(name, ts):
@@ -65,16 +77,6 @@ def _scalar(name, v, device):
             raise ValueError("%s must be a number or one float32 on %s" % (name, device))
         return 0.0, v
     return float(v), None
-
-
-def _table(columns, numels):
-    """Host array of adamw_tensor: `columns` are lists of tensors, or None."""
-    t = np.zeros((len(numels), 8), dtype=np.int64)
-    for k, ts in enumerate(columns):
-        if ts is not None:
-            t[:, k] = np.fromiter(map(_address, ts), np.int64, len(ts))
-    t[:, 7] = numels
-    return t
 
 
 def _workspace(table, device, workspace):
@@ -95,13 +97,13 @@ def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, stream=Non
         raise ValueError("adamw_grad_norm needs at least one gradient")
     device = _gpu_of("grads", grads)
     code = _dtype_code(grads[0].dtype)
-    _check_list("grads", grads, len(grads), grads[0].dtype, device, None)
+    table = _new_table(len(grads))
+    _column(table, _GRAD, "grads", grads, grads[0].dtype, device, 0)
     scale, scale_dev = _scalar("grad_scale", grad_scale, device)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=device)
     else:
         _scalar("norm", norm, device)
-    table = _table([None, grads], list(map(_numel, grads)))
     ws, nws = _workspace(table, device, workspace)
     p = _lib._ptr
     _lib._check(_lib.lib.adamw_grad_norm(code, table.ctypes.data, len(table), scale, p(scale_dev),
@@ -124,30 +126,18 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     if not params:
         return
     device = _gpu_of("params", params)
-    dtype, count = params[0].dtype, len(params)
-    code = _dtype_code(dtype)
-    numels = list(map(_numel, params))
-    _check_list("params", params, count, dtype, device, None)
-    _check_list("grads", grads, count, dtype, device, numels)
+    dtype, code = params[0].dtype, _dtype_code(params[0].dtype)
+    table = _new_table(len(params))
+    _column(table, _PARAM, "params", params, dtype, device, 0)
+    _column(table, _GRAD, "grads", grads, dtype, device)
     state = CODES if scales is not None else torch.float32
-    _check_list("exp_avgs", exp_avgs, count, state, device, numels)
-    _check_list("exp_avg_sqs", exp_avg_sqs, count, state, device, numels)
+    _column(table, _M, "exp_avgs", exp_avgs, state, device)
+    _column(table, _V, "exp_avg_sqs", exp_avg_sqs, state, device)
     if masters is not None:
-        _check_list("masters", masters, count, torch.float32, device, numels)
-    ms = vs = None
+        _column(table, _MASTER, "masters", masters, torch.float32, device)
     if scales is not None:
-        ms, vs = scales
-        blocks = [-(-n // BLOCK) for n in numels]
-        _check_list("scales[0]", ms, count, torch.float32, device, blocks)
-        _check_list("scales[1]", vs, count, torch.float32, device, blocks)
-    _step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas, eps, weight_decay, masters,
-          (ms, vs), numels, code, device, grad_scale, grad_norm, max_norm, workspace, stream)
-
-
-def _step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas, eps, weight_decay, masters,
-          scales, numels, code, device, grad_scale, grad_norm, max_norm, workspace=None, stream=None):
-    """The call, for lists that were checked or are the optimizer's own."""
-    ms, vs = scales
+        _column(table, _M_SCALE, "scales[0]", scales[0], torch.float32, device, BLOCK)
+        _column(table, _V_SCALE, "scales[1]", scales[1], torch.float32, device, BLOCK)
     if not isinstance(step, torch.Tensor) or step.dtype != torch.int32 or step.numel() != 1 or \
             step.device != device:
         raise ValueError("step must be one int32 on %s" % device)
@@ -159,14 +149,13 @@ def _step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas, eps, weight_dec
         if not isinstance(grad_norm, torch.Tensor):
             raise TypeError("grad_norm must be a torch.Tensor")
         _scalar("grad_norm", grad_norm, device)
-    table = _table([params, grads, masters, exp_avgs, exp_avg_sqs, ms, vs], numels)
     ws, nws = _workspace(table, device, workspace)
     p = _lib._ptr
-    config = _lib.AdamwConfig(code, 8 if ms is not None else 32, lr, betas[0], betas[1], eps,
+    config = _lib.AdamwConfig(code, 8 if scales is not None else 32, lr, betas[0], betas[1], eps,
                               weight_decay, scale, max_norm or 0.0, p(lr_dev), p(scale_dev),
                               p(grad_norm))
-    _lib._check(_lib.lib.adamw_step(ctypes.byref(config), table.ctypes.data, len(numels), p(step), p(ws),
-                                    nws, _raw_stream(stream, device)), "adamw_step")
+    _lib._check(_lib.lib.adamw_step(ctypes.byref(config), table.ctypes.data, len(table), p(step),
+                                    p(ws), nws, _raw_stream(stream, device)), "adamw_step")
 
 
 class AdamW(torch.optim.Optimizer):
@@ -273,12 +262,11 @@ class AdamW(torch.optim.Optimizer):
             def column(name):
                 return [s[name] for s in st] if name in st[0] else None
 
-            device, dtype, count = _gpu_of("parameters", ps), ps[0].dtype, len(ps)
-            numels = list(map(_numel, ps))
-            _check_list("parameters", ps, count, dtype, device, None)
-            _check_list("gradients", gs, count, dtype, device, numels)
-            scales = column("exp_avg_scale"), column("exp_avg_sq_scale")
-            _step(ps, gs, column("exp_avg"), column("exp_avg_sq"), step, group["lr"],
-                  group["betas"], group["eps"], group["weight_decay"], column("master"), scales,
-                  numels, _dtype_code(dtype), device, self.grad_scale, norm, self.max_norm)
+            scales = None
+            if self.bits == 8:
+                scales = column("exp_avg_scale"), column("exp_avg_sq_scale")
+            adamw_step(ps, gs, column("exp_avg"), column("exp_avg_sq"), step, lr=group["lr"],
+                       betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
+                       masters=column("master"), scales=scales, grad_scale=self.grad_scale,
+                       grad_norm=norm, max_norm=self.max_norm)
         return loss

@@ -1,12 +1,13 @@
 """Build the HIP library (libwtconv.so) in-tree for gfx950.
 
-    python -m aware_conv_amd.build              # libwtconv.so, valu_probe
+    python -m aware_conv_amd.build              # libwtconv.so, _lists.so, valu_probe
     python -m aware_conv_amd.build --sanitize   # libwtconv_asan.so
 
 compiles every source under ``csrc/`` with hipcc and links one shared object
 next to this file.  Packed-FP32 instruction selection is switched off for the
 device code (``-packed-fp32-ops``); hipcc's host pass warns that it does not
-know that feature, which is harmless.
+know that feature, which is harmless.  ``_lists.so`` (``pyext/``) is a small
+host-only Python extension that reads lists of tensors for the AdamW binding.
 
 ``--sanitize`` builds the same library with the host code (the C-ABI argument
 checks, workspace sizing, dispatch) under AddressSanitizer and
@@ -20,6 +21,7 @@ GPU code is built as usual).  The CPU ABI tests run against it with
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +31,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libwtconv.so")
 PROBE_SRC = os.path.join(CSRC, "probe", "valu_rate.hip")
 PROBE_OUT = os.path.join(HERE, "valu_probe")
+LISTS_SRC = os.path.join(HERE, "pyext", "tensor_lists.cpp")
+LISTS_OUT = os.path.join(HERE, "_lists.so")
 BUILD = os.path.join(HERE, "_build")
 OUT_ASAN = os.path.join(HERE, "libwtconv_asan.so")
 BUILD_ASAN = os.path.join(HERE, "_build_asan")
@@ -61,13 +65,32 @@ def _compile(src, build_dir=BUILD, extra=()):
     return obj
 
 
+def build_lists():
+    """_lists.so against the installed torch; host code only."""
+    import torch
+    from torch.utils import cpp_extension
+    tmp = LISTS_OUT + ".tmp%d" % os.getpid()
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] +
+           ["-isystem" + p for p in cpp_extension.include_paths()] +
+           ["-I" + sysconfig.get_paths()["include"], LISTS_SRC, "-o", tmp,
+            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s%s" % (LISTS_SRC, r.stdout, r.stderr))
+    os.replace(tmp, LISTS_OUT)
+
+
 def build(verbose=True):
     """Compile and link libwtconv.so; always rebuilds."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     workers = max(1, min(len(srcs), int(os.environ.get("MAX_JOBS", "8"))))
     with ThreadPoolExecutor(workers) as ex:
+        lists = ex.submit(build_lists)
         objs = list(ex.map(_compile, srcs))
+        lists.result()
     tmp = OUT + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
