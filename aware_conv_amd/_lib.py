@@ -80,7 +80,7 @@ class AdamwConfig(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("lr_dev", "grad_scale_dev", "norm")])
 
 
-_gp, _gv = ctypes.POINTER(GscanShape), ctypes.POINTER(GscanView)
+_gp, _gv = ctypes.POINTER(GscanShape), _vp  # views: addresses of GscanView
 _szp = ctypes.POINTER(ctypes.c_size_t)
 lib.gscan_states_size.argtypes = [_gp, _szp]
 lib.gscan_workspace_size.argtypes = [_gp, _szp]

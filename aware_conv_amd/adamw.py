@@ -12,13 +12,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from .gscan import _raw_stream
-
-try:
-    from . import _lists
-except ImportError as e:
-    raise ImportError("_lists.so is not built (%s); run `python -m aware_conv_amd.build` or "
-                      "__graft_entry__.build() first" % e)
+from .gscan import _lists, _raw_stream
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 BLOCK = 256

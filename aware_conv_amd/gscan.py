@@ -13,6 +13,12 @@ import torch
 
 from . import _lib
 
+try:
+    from . import _lists
+except ImportError as e:
+    raise ImportError("_lists.so is not built (%s); run `python -m aware_conv_amd.build` or "
+                      "__graft_entry__.build() first" % e)
+
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 LAYOUTS = {"bct": 0, "btc": 1}
 GRAD_NAMES = ("dx", "dr", "di", "dlam", "dh0")
@@ -50,45 +56,58 @@ def _adjacent(t):
     return shape[-1] == 1 or st[-1] == 1
 
 
-# The checks below and the marshalling run once per call and tensor; small calls
-# take about as long as they do, so each is one function per tensor that asks
-# for every attribute once, and pointers go to ctypes as plain integers.
+# Tensors are checked and read by a small extension (pyext/tensor_lists.cpp);
+# what it refuses is looked at again here, to say what is wrong.
 
-def _act(name, t, shape, dtype, device):
-    """The view of an activation that is `shape`, `dtype`, on `device` and has adjacent rows."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype is not dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if not _adjacent(t):
-        raise ValueError("%s must have adjacent elements along its rows" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s; every tensor must be on %s" % (name, t.device, device))
-    st = t.stride()
-    return ctypes.byref(_View(t.data_ptr(), st[0], st[1]))
-
-
-def _flat(name, t, shape, dtype, device):
-    """The address of a contiguous tensor of `shape` and `dtype` on `device`; None for None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s; every tensor must be on %s" % (name, t.device, device))
-    return t.data_ptr()
+def _refuse(names, tensors, flats):
+    """Raises what is wrong with the activations `tensors` (that go by the first, or None) or the
+    contiguous tensors `flats` ((name, tensor, dtype, n0, n1 or -1)): shapes first, devices last."""
+    x = tensors[0]
+    for name, t in zip(names, tensors):
+        if t is None and t is not x and name in _MAY_LACK:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.shape != x.shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(x.shape)))
+        if t.dtype is not x.dtype:
+            raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, x.dtype))
+        if not _adjacent(t):
+            raise ValueError("%s must have adjacent elements along its rows" % name)
+    for name, t, dtype, n0, n1 in flats:
+        if t is None and name in _MAY_LACK:
+            continue
+        _lib._expect(dtype, [(name, t, (n0,) if n1 < 0 else (n0, n1))])
+        if t is None:
+            raise TypeError("%s must be a torch.Tensor" % name)
+    _lib._on_gpu(x, list(zip(names, tensors)) + [f[:2] for f in flats])
+    raise ValueError("tensors of an unsupported kind")
 
 
-_View = _lib.GscanView
+_MAY_LACK = {"h0", "lengths", "dh_last", "slots", "h"} | {"grads[%s]" % n for n in GRAD_NAMES}
 _f32, _i32 = torch.float32, torch.int32
+_VIEW = ctypes.sizeof(_lib.GscanView)
+_Views4, _Views7 = _lib.GscanView * 4, _lib.GscanView * 7
+
+
+def _view(t):
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _read(out, names, tensors, flats):
+    """(address of the views of `tensors` in `out`, addresses of `flats`), checked."""
+    at = ctypes.addressof(out)
+    bad = _lists.views(tensors, at) >= 0
+    device = tensors[0].device.index
+    if not bad:
+        ps = [_lists.flat(t, dtype, device, n0, n1) for _, t, dtype, n0, n1 in flats]
+        # None only where one may lack
+        bad = any(p is False or (p is None and f[0] not in _MAY_LACK) for p, f in zip(ps, flats))
+        # an activation that lacks and may not
+        bad = bad or any(t is None and n not in _MAY_LACK for n, t in zip(names, tensors))
+    if bad:
+        _refuse(names, tensors, flats)
+    return at, ps
 
 
 def _input(x):
@@ -96,11 +115,6 @@ def _input(x):
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     return _dtype_code(x), x.dtype, x.device
-
-
-def _on_gpu(device):
-    if device.type != "cuda":
-        raise ValueError("x is on %s; every tensor must be on a GPU" % device)
 
 
 def _raw_stream(stream, device):
@@ -133,8 +147,11 @@ def _workspace(s, device, workspace):
     if workspace is None:
         need = _sizes(s.B, s.C, s.T, s.layout, s.dtype)[1]
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    p = _flat("workspace", workspace, None, None, device)
-    return workspace, p, workspace.numel() * workspace.element_size()
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    elif workspace.device != device:
+        raise ValueError("workspace is on %s; every tensor must be on %s" % (workspace.device, device))
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def gscan_workspace_size(x, layout="bct"):
@@ -150,24 +167,22 @@ def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, 
     h0 [B, C] are fp32, lengths [B] int32 (see include/gscan.h)."""
     code, dt, dev = _input(x)
     s = _shape(x, code, layout, reverse, decay)
-    shape, rows = x.shape, (s.B, s.C)
-    px, pr, pi = _act("x", x, shape, dt, dev), _act("r", r, shape, dt, dev), _act("i", i, shape, dt, dev)
-    plam = _flat("lam", lam, (s.C,), _f32, dev)
-    ph0 = _flat("h0", h0, rows, _f32, dev)
-    plen = _flat("lengths", lengths, (s.B,), _i32, dev)
-    if h is not None:
-        _act("h", h, shape, dt, dev)
-    _on_gpu(dev)
+    v = _Views4()
+    B, C = s.B, s.C
+    p, (plam, ph0, plen) = _read(v, ("x", "r", "i", "h"), (x, r, i, h),
+                                 (("lam", lam, _f32, C, -1), ("h0", h0, _f32, B, C),
+                                  ("lengths", lengths, _i32, B, -1)))
     if h is None:
-        h = torch.empty(shape, dtype=dt, device=dev)
-    h_last = torch.empty(rows, dtype=_f32, device=dev)
+        h = torch.empty(x.shape, dtype=dt, device=dev)
+        v[3] = _view(h)
+    h_last = torch.empty((B, C), dtype=_f32, device=dev)
     states = pstates = None
     if save_states:
         states = torch.empty(_sizes(s.B, s.C, s.T, s.layout, code)[0], dtype=_f32, device=dev)
         pstates = states.data_ptr()
     ws, pws, nws = _workspace(s, dev, workspace)
-    _lib._check(_lib.lib.gscan_fwd(ctypes.byref(s), px, pr, pi, plam, ph0, plen,
-                                   _act("h", h, shape, dt, dev), h_last.data_ptr(), pstates, pws, nws,
+    _lib._check(_lib.lib.gscan_fwd(ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, ph0, plen,
+                                   p + 3 * _VIEW, h_last.data_ptr(), pstates, pws, nws,
                                    _raw_stream(stream, dev)), "gscan_fwd")
     return h, h_last, states
 
@@ -183,32 +198,31 @@ def gscan_bwd(x, r, i, lam, states, dh, dh_last=None, lengths=None, layout="bct"
         raise KeyError("unknown gradients %s" % ", ".join(map(str, unknown)))
     code, dt, dev = _input(x)
     s = _shape(x, code, layout, reverse, decay)
-    shape, rows = x.shape, (s.B, s.C)
-    px, pr, pi = _act("x", x, shape, dt, dev), _act("r", r, shape, dt, dev), _act("i", i, shape, dt, dev)
-    pdh = _act("dh", dh, shape, dt, dev)
-    plam = _flat("lam", lam, (s.C,), _f32, dev)
-    plast = _flat("dh_last", dh_last, rows, _f32, dev)
-    plen = _flat("lengths", lengths, (s.B,), _i32, dev)
-    for n in ("dx", "dr", "di"):
-        if grads.get(n) is not None:
-            _act("grads[%s]" % n, grads[n], shape, dt, dev)
-    for n, sh in (("dlam", (s.C,)), ("dh0", rows)):
-        _flat("grads[%s]" % n, grads.get(n), sh, _f32, dev)
+    names = ("dx", "dr", "di")
+    v = _Views7()
+    B, C = s.B, s.C
     if states is None:
         raise ValueError("gscan_bwd needs the states of gscan_fwd(..., save_states=True)")
-    pst = _flat("states", states, (_sizes(s.B, s.C, s.T, s.layout, code)[0],), _f32, dev)
-    _on_gpu(dev)
-    for n in ("dx", "dr", "di"):
+    p, (plam, plast, plen, pdlam, pdh0, pst) = _read(
+        v, ("x", "r", "i", "dh", "grads[dx]", "grads[dr]", "grads[di]"),
+        (x, r, i, dh, *[grads.get(n) for n in names]),
+        (("lam", lam, _f32, C, -1), ("dh_last", dh_last, _f32, B, C), ("lengths", lengths, _i32, B, -1),
+         ("grads[dlam]", grads.get("dlam"), _f32, C, -1), ("grads[dh0]", grads.get("dh0"), _f32, B, C),
+         ("states", states, _f32, _sizes(B, C, s.T, s.layout, code)[0], -1)))
+    for k, n in enumerate(names):
         if grads.get(n) is None:
-            grads[n] = torch.empty(shape, dtype=dt, device=dev)
-    for n, sh in (("dlam", (s.C,)), ("dh0", rows)):
-        if grads.get(n) is None:
-            grads[n] = torch.empty(sh, dtype=_f32, device=dev)
+            grads[n] = torch.empty(x.shape, dtype=dt, device=dev)
+            v[4 + k] = _view(grads[n])
+    if pdlam is None:
+        grads["dlam"] = torch.empty(C, dtype=_f32, device=dev)
+        pdlam = grads["dlam"].data_ptr()
+    if pdh0 is None:
+        grads["dh0"] = torch.empty((B, C), dtype=_f32, device=dev)
+        pdh0 = grads["dh0"].data_ptr()
     ws, pws, nws = _workspace(s, dev, workspace)
-    _lib._check(_lib.lib.gscan_bwd(ctypes.byref(s), px, pr, pi, plam, pst, plen, pdh, plast,
-                                   *[_act(n, grads[n], shape, dt, dev) for n in ("dx", "dr", "di")],
-                                   grads["dlam"].data_ptr(), grads["dh0"].data_ptr(), pws, nws,
-                                   _raw_stream(stream, dev)), "gscan_bwd")
+    _lib._check(_lib.lib.gscan_bwd(ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, pst, plen,
+                                   p + 3 * _VIEW, plast, p + 4 * _VIEW, p + 5 * _VIEW, p + 6 * _VIEW,
+                                   pdlam, pdh0, pws, nws, _raw_stream(stream, dev)), "gscan_bwd")
     return grads
 
 
@@ -217,25 +231,25 @@ def gscan_step(x, r, i, lam, state, slots=None, decay=8.0, h=None, stream=None):
     ``slots`` (int32 [B]; the first B rows if None) of ``state`` [S, C] fp32, which is updated.
     Returns h [B, C].  Sequences whose slot is outside 0..S-1 give zeros and change nothing."""
     code, dt, dev = _input(x)
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError("activations must be [B, C], got shape %s" % (tuple(shape),))
-    B, C = shape
-    px, pr, pi = _act("x", x, shape, dt, dev), _act("r", r, shape, dt, dev), _act("i", i, shape, dt, dev)
-    plam = _flat("lam", lam, (C,), _f32, dev)
-    pstate = _flat("state", state, None, _f32, dev)
+    if x.dim() != 2:
+        raise ValueError("activations must be [B, C], got shape %s" % (tuple(x.shape),))
+    B, C = x.shape
+    if not isinstance(state, torch.Tensor):
+        raise TypeError("state must be a torch.Tensor")
     if state.dim() != 2 or state.shape[1] != C:
         raise ValueError("state must be [S, %d], got shape %s" % (C, tuple(state.shape)))
     S = state.shape[0]
-    pslots = _flat("slots", slots, (B,), _i32, dev)
     if slots is None and S < B:
         raise ValueError("state has %d rows for %d sequences" % (S, B))
-    _on_gpu(dev)
+    v = _Views4()
+    p, (plam, pstate, pslots) = _read(v, ("x", "r", "i", "h"), (x, r, i, h),
+                                      (("lam", lam, _f32, C, -1), ("state", state, _f32, S, C),
+                                       ("slots", slots, _i32, B, -1)))
     if h is None:
-        h = torch.empty(shape, dtype=dt, device=dev)
-    _lib._check(_lib.lib.gscan_step(B, C, S, code, decay, px, pr, pi, plam, pstate, pslots,
-                                    _act("h", h, shape, dt, dev), _raw_stream(stream, dev)),
-                "gscan_step")
+        h = torch.empty((B, C), dtype=dt, device=dev)
+        v[3] = _view(h)
+    _lib._check(_lib.lib.gscan_step(B, C, S, code, decay, p, p + _VIEW, p + 2 * _VIEW, plam, pstate,
+                                    pslots, p + 3 * _VIEW, _raw_stream(stream, dev)), "gscan_step")
     return h
 
 

@@ -1,9 +1,11 @@
-// Python extension of the AdamW binding (aware_conv_amd/adamw.py): checks the
-// tensors of a list and writes their addresses into a host table, in one call.
+// Python extension of the bindings in aware_conv_amd/adamw.py and gscan.py:
+// checks tensors and reads what the library takes of them, in one call for
+// several tensors.  What is wrong is put into words by the caller.
 //
 // A step over a hundred small tensors has several hundred of them to check and
 // look up; attribute by attribute from Python that takes longer than the step
-// itself does on the GPU (96 us for 90 tensors of 4 lists; the GPU takes 13).
+// itself does on the GPU (96 us for 90 tensors of 4 lists; the GPU takes 13),
+// and a single decoded token's call is mostly that, too.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -66,7 +68,69 @@ PyObject* column(PyObject*, PyObject* args) {
     return Py_BuildValue("in", code, i);
 }
 
-PyMethodDef methods[] = {{"column", column, METH_VARARGS, "Checks a list of tensors and writes their addresses."},
+// Whether each row (the last axis; the planes of a 4-D tensor) is one run.
+bool adjacent(const at::Tensor& t) {
+    if (t.is_contiguous() || t.numel() == 0) return true;
+    const int64_t n = t.dim();
+    if (n == 4 && !(t.size(2) == 1 || t.stride(2) == t.size(3))) return false;
+    return t.size(n - 1) == 1 || t.stride(n - 1) == 1;
+}
+
+// views(tensors, address) -> index of the first that does not fit, or -1
+//
+// tensors: a tuple whose first is a CUDA tensor of two to four axes; the others
+// are None or of its shape, dtype and device, and all have adjacent rows.
+// Writes (pointer, stride of axis 0, stride of axis 1) of each, 64 bits each;
+// zeros for None.
+PyObject* views(PyObject*, PyObject* args) {
+    PyObject* tuple;
+    unsigned long long address;
+    if (!PyArg_ParseTuple(args, "O!K", &PyTuple_Type, &tuple, &address)) return nullptr;
+    long long* out = reinterpret_cast<long long*>(address);
+    const Py_ssize_t n = PyTuple_GET_SIZE(tuple);
+    const at::Tensor* x = nullptr;
+    for (Py_ssize_t i = 0; i < n; ++i, out += 3) {
+        PyObject* o = PyTuple_GET_ITEM(tuple, i);
+        if (i > 0 && o == Py_None) {
+            out[0] = out[1] = out[2] = 0;
+            continue;
+        }
+        if (!THPVariable_Check(o)) return PyLong_FromSsize_t(i);
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (i == 0) x = &t;
+        if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() < 2 || t.dim() > 4 ||
+            t.scalar_type() != x->scalar_type() || t.device() != x->device() ||
+            t.sizes() != x->sizes() || !adjacent(t))
+            return PyLong_FromSsize_t(i);
+        out[0] = reinterpret_cast<long long>(t.data_ptr());
+        out[1] = t.stride(0);
+        out[2] = t.stride(1);
+    }
+    return PyLong_FromLong(-1);
+}
+
+// flat(tensor, dtype, device, n0, n1) -> address, None for None, False if it
+// does not fit: contiguous, of that dtype on that CUDA device, of the shape
+// (n0, n1), or (n0,) for a negative n1.
+PyObject* flat(PyObject*, PyObject* args) {
+    PyObject *o, *dtype;
+    int device;
+    long long n0, n1;
+    if (!PyArg_ParseTuple(args, "OOiLL", &o, &dtype, &device, &n0, &n1)) return nullptr;
+    if (o == Py_None) Py_RETURN_NONE;
+    if (!THPVariable_Check(o) || !THPDtype_Check(dtype)) Py_RETURN_FALSE;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    const int dims = n1 < 0 ? 1 : 2;
+    if (t.scalar_type() != reinterpret_cast<THPDtype*>(dtype)->scalar_type || !t.is_cuda() ||
+        t.device().index() != device || t.layout() != at::kStrided || t.dim() != dims ||
+        t.size(0) != n0 || (dims == 2 && t.size(1) != n1) || !t.is_contiguous())
+        Py_RETURN_FALSE;
+    return PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.data_ptr()));
+}
+
+PyMethodDef methods[] = {{"views", views, METH_VARARGS, "Checks strided activations and writes their views."},
+                         {"flat", flat, METH_VARARGS, "Checks a contiguous tensor and returns its address."},
+                         {"column", column, METH_VARARGS, "Checks a list of tensors and writes their addresses."},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
