@@ -5,6 +5,9 @@
 // nothing is copied or kept, and a captured launch keeps its own); a workgroup
 // takes one chunk of one tensor.  The step is bound by HBM: it reads and
 // writes each value once, 16 bytes per lane and access where the type allows.
+// 94M elements in fp32: 510 us, 5.2 TB/s; 140M in bf16 with masters and 8-bit
+// moments 420 us, 5.3 TB/s (a large copy reaches 4.94 TB/s).  Ninety tensors of
+// 1.06M elements together take 10 us, mostly launch latency.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -132,7 +135,9 @@ __device__ __forceinline__ float finite_abs(float v) {
     return a <= 3e38f ? a : 0.f;
 }
 
-// Codes and scale of a block of the wavefront (four elements per lane).
+// Codes and scale of a block of the wavefront (four elements per lane): 256
+// elements, so that the block's largest magnitude takes six lane exchanges and
+// no LDS, and the scales add 1/32 of a byte to an element's 16.
 template <bool ROOT>
 __device__ __forceinline__ uint32_t encode(const float (&v)[kVec], uint32_t k, uint32_t turn,
                                            float& scale) {
@@ -276,6 +281,8 @@ __global__ __launch_bounds__(kThreads) void k_step(
     }
 }
 
+// Partial sums of squares: 140M bf16 elements in 61 us (4.6 TB/s) where they
+// come from HBM at a stretch.
 template <class D>
 __global__ __launch_bounds__(kThreads) void k_squares(Table<1, kFit<1>> t, double* part) {
     using S = typename D::S;

@@ -8,6 +8,18 @@
 // again from the state that it then knows.  The state passes from tile to tile
 // between workgroups (gscan_carry.h).  Everything is read once and written
 // once.
+//
+// What bounds it (8x4096x2048, against a large copy's 4.94 TB/s): in fp32 HBM
+// (210 us forwards, 5.1 TB/s; 397 us backwards, 4.7 TB/s); in bf16, with half
+// the bytes for the same arithmetic, the vector ALU is busy for 57% of the
+// forward (132 us, 4.1 TB/s) and 51% of the backward (245 us, 3.8 TB/s) and
+// the rest is the tile's latency chain: counter, loads, LDS, the wait for the
+// tiles before.  16 positions per thread amortise the address and LDS work
+// (8: 145 and 304 us); 8 threads along time backwards hold 32 elements in up
+// to 256 registers, two workgroups to a unit, which beats more threads of
+// fewer registers (512 threads of 16 elements: 304 us).  Wider tiles (128
+// channels) and workgroups that stay and fetch their next unit early were
+// slower (267 and 293 us backwards).
 #include <hip/hip_runtime.h>
 
 #include "gscan_math.h"
@@ -468,33 +480,48 @@ __global__ __launch_bounds__(kCloseChan* kCloseRows) void k_close_dlam(Args g, l
     }
 }
 
-template <class D>
-__global__ __launch_bounds__(256) void k_step(int C, int S, const typename D::S* x, long long xs,
-                                              const typename D::S* r, long long rs,
+// One position: a thread takes two channels of R sequences, whose loads are
+// under way together and which share the channels' rates.  512 x 4096 bf16: 7.2
+// us, 4.6 TB/s; a single sequence of 384 channels 2.0 us, a launch's latency.
+template <class D, int R>
+__global__ __launch_bounds__(256) void k_step(int B, int C, int S, const typename D::S* x,
+                                              long long xs, const typename D::S* r, long long rs,
                                               const typename D::S* i, long long is,
                                               const float* lam, float decay, float* state,
                                               const int* slots, typename D::S* h, long long hs) {
     const unsigned wide = (C + 511) / 512;
-    const long long b = blockIdx.x / wide;
+    const int b0 = int(blockIdx.x / wide) * R;
     const int c = ((blockIdx.x % wide) * 256 + threadIdx.x) * 2;
     const int n = min(C - c, 2);
     if (n <= 0) return;
-    const int slot = slots ? slots[b] : int(b);
-    const bool on = slot >= 0 && slot < S;
-    const Raw<D, 2> qx = fetch2<D>(x + b * xs + c, on ? n : 0);
-    const Raw<D, 2> qr = fetch2<D>(r + b * rs + c, on ? n : 0);
-    const Raw<D, 2> qi = fetch2<D>(i + b * is + c, on ? n : 0);
-    float out[2] = {0.f, 0.f};
+    int slot[R];
+    Raw<D, 2> qx[R], qr[R], qi[R];
+    Raw<F32, 2> qs[R];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (!on || e >= n) continue;
-        float a, v, sr, si;
-        gate_fwd(qx.get(e), qr.get(e), qi.get(e), rate_of(decay, lam[c + e]), a, v, sr, si);
-        float* s = state + (long long)slot * C + c + e;
-        out[e] = fmaf(a, *s, v);
-        *s = out[e];
+    for (int k = 0; k < R; ++k) {
+        const int b = b0 + k;
+        slot[k] = b < B ? (slots ? slots[b] : b) : -1;
+        const int m = slot[k] >= 0 && slot[k] < S ? n : 0;
+        qx[k] = fetch2<D>(x + b * xs + c, m);
+        qr[k] = fetch2<D>(r + b * rs + c, m);
+        qi[k] = fetch2<D>(i + b * is + c, m);
+        qs[k] = fetch2<F32>(state + (long long)slot[k] * C + c, m);
     }
-    put2<D>(h + b * hs + c, out[0], out[1], n);
+    const float rate[2] = {rate_of(decay, lam[c]), n > 1 ? rate_of(decay, lam[c + 1]) : 0.f};
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        float out[2] = {0.f, 0.f};
+        if (slot[k] >= 0 && slot[k] < S) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float a, v, sr, si;
+                gate_fwd(qx[k].get(e), qr[k].get(e), qi[k].get(e), rate[e], a, v, sr, si);
+                out[e] = fmaf(a, qs[k].get(e), v);
+            }
+            put2<F32>(state + (long long)slot[k] * C + c, out[0], out[1], n);
+        }
+        if (b0 + k < B) put2<D>(h + (b0 + k) * hs + c, out[0], out[1], n);
+    }
 }
 
 // Sequences of one tile take a tile as long as they need; else tiles of kLen
@@ -592,13 +619,19 @@ hipError_t close_dlam(const Args& a, long long parts, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Sequences of a thread: one while the threads are too few to fill the device
+// (latency), else four (one and four: 256 x 2048 bf16 3.4 and 4.2 us, 512 x 4096
+// 7.3 and 7.2, 2048 x 4096 23.5 and 21.9).
 template <class D>
 static void launch_step(int B, int C, int S, float decay, const gscan_view& x, const gscan_view& r,
                         const gscan_view& i, const float* lam, float* state, const int* slots,
                         const gscan_view& h, hipStream_t st) {
     using E = typename D::S;
-    k_step<D><<<dim3((C + 511) / 512 * unsigned(B)), 256, 0, st>>>(
-        C, S, static_cast<const E*>(x.p), x.sb, static_cast<const E*>(r.p), r.sb,
+    const bool many = (long long)B * C >= 1 << 21;
+    const unsigned rows = many ? (B + 3) / 4 : B;
+    auto* kernel = many ? k_step<D, 4> : k_step<D, 1>;
+    kernel<<<dim3((C + 511) / 512 * rows), 256, 0, st>>>(
+        B, C, S, static_cast<const E*>(x.p), x.sb, static_cast<const E*>(r.p), r.sb,
         static_cast<const E*>(i.p), i.sb, lam, decay, state, slots, static_cast<E*>(h.p), h.sb);
 }
 
