@@ -12,7 +12,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from .gscan import _lists, _raw_stream
+from .gscan import _lists, _raw_stream, on_stream
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 BLOCK = 256
@@ -84,7 +84,8 @@ def _workspace(table, device, workspace):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, stream=None):
+@on_stream
+def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, *, stream=None):
     """2-norm of ``grad_scale`` times all gradients together, as one fp32 on the device."""
     grads = list(grads)
     if not grads:
@@ -106,9 +107,10 @@ def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, stream=Non
     return norm
 
 
+@on_stream
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                weight_decay=0.01, masters=None, scales=None, grad_scale=1.0, grad_norm=None,
-               max_norm=None, workspace=None, stream=None):
+               max_norm=None, workspace=None, *, stream=None):
     """One AdamW step over lists of tensors, in place.
 
     step: int32 on the device, the steps taken so far (advanced).  masters: fp32 copies of the

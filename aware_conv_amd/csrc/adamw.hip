@@ -294,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void k_squares(Table<1, kFit<1>> t, doubl
     // fp64 from the first product: the sum of squares of fp32 values may leave
     // fp32's range, and the conversion costs less than the memory access
     double s = 0;
-#pragma unroll 4
+#pragma unroll
     for (int u = 0; u < int(kNormChunk) / (kThreads * kVec); ++u) {
         const long long k = base + (u * kThreads + threadIdx.x) * kVec;
         const int left = int(n - k < kVec ? (n - k > 0 ? n - k : 0) : kVec);

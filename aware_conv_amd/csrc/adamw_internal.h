@@ -20,7 +20,7 @@ struct Ctl {
 };
 
 constexpr size_t kCtlBytes = 64;
-constexpr long long kNormChunk = 16384;  // elements of a partial sum of squares
+constexpr long long kNormChunk = 8192;  // elements of a partial sum of squares
 
 hipError_t grad_norm(int dtype, const adamw_tensor* t, int count, double scale,
                      const float* scale_dev, float* norm, double* part, hipStream_t st);

@@ -117,6 +117,19 @@ def _input(x):
     return _dtype_code(x), x.dtype, x.device
 
 
+def on_stream(call):
+    """A call given a stream that is not the current one runs with it as the current one: what it
+    allocates then belongs to that stream, and is not handed out again while its kernels use it."""
+    @functools.wraps(call)
+    def wrapped(*args, **kw):
+        stream = kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return wrapped
+
+
 def _raw_stream(stream, device):
     """The stream's handle; without a stream, that of the current one, as an integer (a Stream
     object would cost as much as the rest of a small call's marshalling)."""
@@ -160,8 +173,9 @@ def gscan_workspace_size(x, layout="bct"):
     return _sizes(B, C, T, LAYOUTS[layout], _dtype_code(x))[1]
 
 
+@on_stream
 def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, decay=8.0, h=None,
-              save_states=False, workspace=None, stream=None):
+              save_states=False, workspace=None, *, stream=None):
     """(h, h_last, states) of the recurrence: h like x, h_last [B, C] fp32 the state after the
     last valid position, states what gscan_bwd needs (None unless ``save_states``).  lam [C] and
     h0 [B, C] are fp32, lengths [B] int32 (see include/gscan.h)."""
@@ -187,8 +201,9 @@ def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, 
     return h, h_last, states
 
 
+@on_stream
 def gscan_bwd(x, r, i, lam, states, dh, dh_last=None, lengths=None, layout="bct", reverse=False,
-              decay=8.0, grads=None, workspace=None, stream=None):
+              decay=8.0, grads=None, workspace=None, *, stream=None):
     """Gradients of <dh, h> + <dh_last, h_last> as a dict keyed by GRAD_NAMES, from the inputs
     and the states of gscan_fwd.  ``grads`` may hold tensors to write (dx, dr, di with free
     strides); those it lacks are allocated."""
@@ -226,7 +241,8 @@ def gscan_bwd(x, r, i, lam, states, dh, dh_last=None, lengths=None, layout="bct"
     return grads
 
 
-def gscan_step(x, r, i, lam, state, slots=None, decay=8.0, h=None, stream=None):
+@on_stream
+def gscan_step(x, r, i, lam, state, slots=None, decay=8.0, h=None, *, stream=None):
     """One position of B sequences: x, r, i [B, C] (free row strides), their states in rows
     ``slots`` (int32 [B]; the first B rows if None) of ``state`` [S, C] fp32, which is updated.
     Returns h [B, C].  Sequences whose slot is outside 0..S-1 give zeros and change nothing."""
@@ -275,6 +291,7 @@ class GatedScanFunction(torch.autograd.Function):
         return h, h_last
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dh_last):
         x, r, i, lam, lengths, states = ctx.saved_tensors
         if dh is None:

@@ -357,3 +357,33 @@ def test_graph_and_streams(layout, B, C, T):
     torch.cuda.synchronize()
     for run in got:
         assert all(torch.equal(a, b) for a, b in zip(run, want))
+
+
+def test_a_stream_of_its_own():
+    """Calls given a stream: their workspace must not be handed out again, on the current stream,
+    while they run."""
+    import aware_conv_amd as A
+    d = make(2, 70, 3000, "f32", "btc", 16)
+    form = {"layout": "btc"}
+    h, _, st = A.gscan_fwd(d["x"], d["r"], d["i"], d["lam"], save_states=True, **form)
+    want = [h] + list(A.gscan_bwd(d["x"], d["r"], d["i"], d["lam"], st, d["dh"], **form).values())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        h, _, st = A.gscan_fwd(d["x"], d["r"], d["i"], d["lam"], save_states=True, stream=side, **form)
+        g = A.gscan_bwd(d["x"], d["r"], d["i"], d["lam"], st, d["dh"], stream=side, **form)
+        # on the current stream, as large as the workspaces were
+        junk = [torch.full((1 << 20,), 0x5a, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip([h] + list(g.values()), want))
+        del junk
+
+
+def test_second_derivatives_are_refused():
+    import aware_conv_amd as A
+    d = make(1, 2, 9, "f32", "bct", 17)
+    x = d["x"].clone().requires_grad_()
+    h = A.gated_scan(x, d["r"], d["i"], d["lam"])[0]
+    g, = torch.autograd.grad(h.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()

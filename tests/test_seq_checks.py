@@ -208,9 +208,9 @@ def test_norm_arguments():
     assert norm(dtype=9) == DTYPE and norm(count=-1) == SHAPE and norm(scale=float("inf")) == VALUE
     assert norm(t=table(g=None)) == NULL and norm(t=table(g=far(1) + 2)) == ALIGN
     assert norm(out=None) == NULL and norm(out=far(50) + 2) == ALIGN
-    # 16384 elements to a partial sum
+    # 8192 elements to a partial sum
     n = ctypes.c_size_t(0)
-    t = table(n=16385 * 16384)
+    t = table(n=16385 * 8192)
     assert L.lib.adamw_workspace_size(t.ctypes.data, 2, ctypes.byref(n)) == 0 and n.value == 8 * 16386
     assert L.lib.adamw_workspace_size(t.ctypes.data, 2, None) == NULL
 
