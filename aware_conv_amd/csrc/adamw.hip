@@ -6,7 +6,7 @@
 // takes one chunk of one tensor.  The step is bound by HBM: it reads and
 // writes each value once, 16 bytes per lane and access where the type allows.
 // 94M elements in fp32: 510 us, 5.2 TB/s; 140M in bf16 with masters and 8-bit
-// moments 420 us, 5.3 TB/s (a large copy reaches 4.94 TB/s).  Ninety tensors of
+// moments 403 us, 5.6 TB/s (a large copy reaches 4.94 TB/s).  Ninety tensors of
 // 1.06M elements together take 10 us, mostly launch latency.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -42,16 +42,20 @@ struct Table {
 template <int P>
 constexpr int kFit = (4096 - 96) / (8 * P + 8 + 4);
 
-// The tensor that holds chunk `blk`.
+// The tensor that holds chunk `blk`: the number of tensors after the first
+// that start at it or before.  The lanes compare all starts at once; a binary
+// search would wait for one kernel argument after the other (the step over 90
+// tensors: 9.8 us, now 9.2).
 template <int P, int N>
 __device__ __forceinline__ int tensor_of(const Table<P, N>& t, int blk) {
-    int lo = 0, hi = t.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (t.first[mid] <= blk) lo = mid;
-        else hi = mid - 1;
+    const int lane = threadIdx.x & 63;
+    int id = 0;
+#pragma unroll
+    for (int k = 1; k < N; k += 64) {
+        const int i = k + lane;
+        id += __popcll(__ballot(i < t.count && t.first[i < N ? i : 0] <= blk));
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(id);
 }
 
 template <class D>
@@ -111,11 +115,22 @@ __device__ __forceinline__ void decode(uint32_t w, float (&v)[kVec]) {
     v[3] = hi[1];
 }
 
-// Largest of the wavefront's non-negative values, in every lane.
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+// Largest of the wavefront's non-negative values, in every lane: DPP moves (six
+// instructions; lane exchanges through LDS would wait for each other six
+// times), compared as integers, whose order is the same.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int max_from(int v) {
+    return max(v, __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float wave_max(float f) {
+    int v = __float_as_int(f);
+    v = max_from<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8
+    v = max_from<0x112, 0xf>(v);
+    v = max_from<0x114, 0xf>(v);
+    v = max_from<0x118, 0xf>(v);
+    v = max_from<0x142, 0xa>(v);  // row_bcast:15, 31
+    v = max_from<0x143, 0xc>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(v, 63));
 }
 
 // The magnitude's code (as the value it stands for) for x >= 0 in units of the
@@ -210,74 +225,106 @@ enum { P_, G_, M_, V_, X0_ };  // then: master, and/or the two scales
 template <class D, bool BITS8, bool MASTER>
 constexpr int kPtrs = 4 + (MASTER ? 1 : 0) + (BITS8 ? 2 : 0);
 
+// What a lane reads of one unit, as loaded.
+template <class D, bool BITS8, bool MASTER>
+struct In {
+    Raw<D, kVec> g, p;
+    Raw<F32, kVec> w, m, v;  // v, m: moments in 32 bits
+    uint32_t cm, cv;         // codes
+    float sm, sv;            // and their scales
+};
+
+// The loads of a batch of units come before its first store: a store could, for
+// all the compiler knows, change what a later load reads, and the loads would
+// wait for one another, unit by unit.  94M elements in fp32: 515 us unit by
+// unit, 509 with all four at once; 140M with 8-bit moments and masters 413 unit
+// by unit, 402 in pairs, 402 with four at once (and 18 us in place of 16.5 for
+// 37 small tensors, whose registers four at once double).
 template <class D, bool BITS8, bool MASTER>
 __global__ __launch_bounds__(kThreads) void k_step(
     Table<kPtrs<D, BITS8, MASTER>, kFit<kPtrs<D, BITS8, MASTER>>> t, const Ctl* ctl, Betas h) {
     using S = typename D::S;
-    const Ctl c = *ctl;
-    if (!c.on) return;
+    using St = std::conditional_t<BITS8, uint8_t, float>;
     const int id = tensor_of(t, blockIdx.x);
     const long long n = t.n[id];
     const long long base = (long long)(int(blockIdx.x) - t.first[id]) * kChunk;
     S* p = static_cast<S*>(t.ptr[P_][id]);
     const S* g = static_cast<const S*>(t.ptr[G_][id]);
+    St* m = static_cast<St*>(t.ptr[M_][id]);
+    St* v = static_cast<St*>(t.ptr[V_][id]);
     float* w = MASTER ? static_cast<float*>(t.ptr[X0_][id]) : nullptr;
+    float* ms = BITS8 ? static_cast<float*>(t.ptr[X0_ + MASTER][id]) : nullptr;
+    float* vs = BITS8 ? static_cast<float*>(t.ptr[X0_ + MASTER + BITS8][id]) : nullptr;
+    auto at = [&](int u) { return base + (u * kThreads + threadIdx.x) * kVec; };
+    auto left = [&](int u) {
+        const long long r = n - at(u);
+        return int(r < kVec ? (r > 0 ? r : 0) : kVec);
+    };
+    // a wavefront's 256 elements are one block
+    auto block = [&](int u) { return (base + (u * kThreads + threadIdx.x / 64 * 64) * kVec) / ADAMW_BLOCK; };
+    constexpr int kBatch = BITS8 ? 2 : kUnits;
+    const Ctl c = *ctl;
+    if (!c.on) return;
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        const long long k = base + (u * kThreads + threadIdx.x) * kVec;
-        const int left = int(n - k < kVec ? (n - k > 0 ? n - k : 0) : kVec);
-        const Raw<D, kVec> qg = fetch<D>(g + k, left);
-        float pv[kVec], mv[kVec], vv[kVec], sv[kVec];
-        if constexpr (MASTER) {
-            const Raw<F32, kVec> qw = fetch<F32>(w + k, left);
+    for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
+        In<D, BITS8, MASTER> in[kBatch];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) pv[j] = qw.get(j);
-        } else {
-            const Raw<D, kVec> qp = fetch<D>(p + k, left);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) pv[j] = qp.get(j);
+        for (int u = u0; u < u0 + kBatch; ++u) {
+            In<D, BITS8, MASTER>& q = in[u - u0];
+            const long long k = at(u);
+            const int l = left(u);
+            q.g = fetch<D>(g + k, l);
+            if constexpr (MASTER) q.w = fetch<F32>(w + k, l);
+            else q.p = fetch<D>(p + k, l);
+            if constexpr (BITS8) {
+                const bool any = block(u) * ADAMW_BLOCK < n;
+                q.cm = fetch_codes(m + k, l);
+                q.cv = fetch_codes(v + k, l);
+                q.sm = any ? ms[block(u)] : 0.f;
+                q.sv = any ? vs[block(u)] : 0.f;
+            } else {
+                q.m = fetch<F32>(m + k, l);
+                q.v = fetch<F32>(v + k, l);
+            }
         }
-        if constexpr (BITS8) {
-            uint8_t* m = static_cast<uint8_t*>(t.ptr[M_][id]);
-            uint8_t* v = static_cast<uint8_t*>(t.ptr[V_][id]);
-            float* ms = static_cast<float*>(t.ptr[X0_ + MASTER][id]);
-            float* vs = static_cast<float*>(t.ptr[X0_ + MASTER + 1][id]);
-            // a wavefront's 256 elements are one block
-            const long long blk = (base + (u * kThreads + threadIdx.x / 64 * 64) * kVec) / ADAMW_BLOCK;
-            const bool any = blk * ADAMW_BLOCK < n;
-            const float sm = any ? ms[blk] : 0.f, sr = any ? vs[blk] : 0.f;
-            decode(fetch_codes(m + k, left), mv);
-            decode(fetch_codes(v + k, left), vv);
+#pragma unroll
+        for (int u = u0; u < u0 + kBatch; ++u) {
+            const In<D, BITS8, MASTER>& q = in[u - u0];
+            const long long k = at(u);
+            const int l = left(u);
+            float pv[kVec], mv[kVec], vv[kVec], sv[kVec];
+            if constexpr (BITS8) {
+                decode(q.cm, mv);
+                decode(q.cv, vv);
+            }
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                vv[j] *= sr;
-                vv[j] *= vv[j];
-                advance(pv[j], mv[j], sm, mv[j], vv[j], qg.get(j), c, h, sv[j]);
+                if constexpr (MASTER) pv[j] = q.w.get(j);
+                else pv[j] = q.p.get(j);
+                if constexpr (BITS8) {
+                    vv[j] *= q.sv;
+                    vv[j] *= vv[j];
+                    advance(pv[j], mv[j], q.sm, mv[j], vv[j], q.g.get(j), c, h, sv[j]);
+                } else {
+                    vv[j] = q.v.get(j);
+                    advance(pv[j], q.m.get(j), 1.f, mv[j], vv[j], q.g.get(j), c, h, sv[j]);
+                }
             }
-            float a, b;
-            const uint32_t cm = encode<false>(mv, uint32_t(k), c.turn, a);
-            const uint32_t cv = encode<true>(sv, uint32_t(k), c.turn, b);
-            put_codes(m + k, cm, left);
-            put_codes(v + k, cv, left);
-            if (any && threadIdx.x % 64 == 0) {
-                ms[blk] = a;
-                vs[blk] = b;
+            if constexpr (BITS8) {
+                float a, b;
+                put_codes(m + k, encode<false>(mv, uint32_t(k), c.turn, a), l);
+                put_codes(v + k, encode<true>(sv, uint32_t(k), c.turn, b), l);
+                if (block(u) * ADAMW_BLOCK < n && threadIdx.x % 64 == 0) {
+                    ms[block(u)] = a;
+                    vs[block(u)] = b;
+                }
+            } else {
+                put<F32>(m + k, mv, l);
+                put<F32>(v + k, vv, l);
             }
-        } else {
-            float* m = static_cast<float*>(t.ptr[M_][id]);
-            float* v = static_cast<float*>(t.ptr[V_][id]);
-            const Raw<F32, kVec> qm = fetch<F32>(m + k, left), qv = fetch<F32>(v + k, left);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                mv[j] = qm.get(j);
-                vv[j] = qv.get(j);
-                advance(pv[j], mv[j], 1.f, mv[j], vv[j], qg.get(j), c, h, sv[j]);
-            }
-            put<F32>(m + k, mv, left);
-            put<F32>(v + k, vv, left);
+            if constexpr (MASTER) put<F32>(w + k, pv, l);
+            put<D>(p + k, pv, l);
         }
-        if constexpr (MASTER) put<F32>(w + k, pv, left);
-        put<D>(p + k, pv, left);
     }
 }
 
