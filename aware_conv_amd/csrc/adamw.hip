@@ -135,8 +135,9 @@ __device__ __forceinline__ float wave_max(float f) {
 
 // The magnitude's code (as the value it stands for) for x >= 0 in units of the
 // scale and dither d.  Codes are 8 steps per power of two down to 2^-6, and
-// evenly spaced below.  x / ulp is exact (ulp is a power of two), below 16, so
-// adding d loses at most 2^-21 of a step.
+// evenly spaced below.  x / ulp is exact (ulp is a power of two), so its sum
+// with d is rounded once, as adamw.h says: it is below 16, and a decision is
+// off by at most 2^-21 of a step.
 __device__ __forceinline__ float code_of(float x, float d) {
     const uint32_t e = max(__float_as_uint(x) & 0x7f800000u, 0x3c800000u);  // 2^exponent, at least 2^-6
     const float ulp = __uint_as_float(e - (3u << 23));
@@ -152,14 +153,15 @@ __device__ __forceinline__ float finite_abs(float v) {
 
 // Codes and scale of a block of the wavefront (four elements per lane): 256
 // elements, so that the block's largest magnitude takes six lane exchanges and
-// no LDS, and the scales add 1/32 of a byte to an element's 16.
+// no LDS, and the scales add 1/32 of a byte to an element's 16.  Every
+// operation is one that adamw.h names, rounded by itself.
 template <bool ROOT>
 __device__ __forceinline__ uint32_t encode(const float (&v)[kVec], uint32_t k, uint32_t turn,
                                            float& scale) {
     float top = 0.f;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) top = fmaxf(top, finite_abs(v[j]));
-    scale = wave_max(top) / 448.f;  // rounded once: a block's codes all go by it
+    scale = wave_max(top) * (1.f / 448.f);
     const bool live = scale >= 1.17549435e-38f;
     scale = live ? scale : 0.f;
     const float inv = live ? 1.f / scale : 0.f;
@@ -187,10 +189,14 @@ __global__ void k_begin(int* step, const float* lr_dev, const float* scale_dev, 
     if (lr_dev) lr = double(*lr_dev);
     if (scale_dev) scale = double(*scale_dev);
     c.on = 1;
+    c.factor = float(scale);
     if (norm) {
         const float n = *norm;
         c.on = fabsf(n) <= 3.4028235e38f;
-        if (max_norm > 0) scale *= fmin(1.0, max_norm / (double(n) + 1e-6));
+        if (max_norm > 0) {
+            scale *= fmin(1.0, max_norm / (double(n) + 1e-6));
+            c.factor *= fminf(1.f, float(max_norm) / (n + 1e-6f));
+        }
     }
     c.keep = float(1.0 - lr * decay);
     c.rate = float(lr / (1.0 - pow(beta1, double(t))));
@@ -204,20 +210,43 @@ __global__ void k_begin(int* step, const float* lr_dev, const float* scale_dev, 
 struct Betas {
     double b1, o1;  // o = 1 - b
     float b2, o2, eps;
+    float b1f, o1f;  // b1 and o1, rounded
 };
 
-// New moments and parameter of one element; m0 is factor * scale.  The two
-// terms of m may cancel, which would leave an fp32 sum with few of its digits
-// for a parameter whose v is small: m is formed in fp64, whose few
-// instructions hide behind the memory accesses, and rounded once.
-__device__ __forceinline__ void advance(float& p, float factor, float scale, float& m, float& v,
-                                        float g, const Ctl& c, const Betas& h, float& s) {
+// The two terms of m may cancel, which would leave an fp32 sum with few of its
+// digits for a parameter whose v is small: the m that moves the parameter is
+// formed in fp64, whose few instructions hide behind the memory accesses, and
+// rounded once.
+__device__ __forceinline__ void move(float& p, float m, float s, const Ctl& c, const Betas& h) {
+    p = fmaf(p, c.keep, -c.rate * m * gsc::rcp_hw(fmaf(s, c.root, h.eps)));
+}
+
+// New moments and parameter of one element.
+__device__ __forceinline__ void advance(float& p, float& m, float& v, float g, const Ctl& c,
+                                        const Betas& h) {
     const double gd = double(g) * c.scale;
-    m = float(fma(h.b1, double(factor) * double(scale), h.o1 * gd));
+    m = float(fma(h.b1, double(m), h.o1 * gd));
     g = float(gd);
     v = fmaf(h.b2, v, (h.o2 * g) * g);
-    s = gsc::sqrt_hw(v);
-    p = fmaf(p, c.keep, -c.rate * m * gsc::rcp_hw(fmaf(s, c.root, h.eps)));
+    move(p, m, gsc::sqrt_hw(v), c, h);
+}
+
+// The same with moments in 8 bits: m and s are the values of the codes, then
+// what is to be encoded.  A code changes by 6 to 12 % where its value crosses a
+// decision by one unit in the last place, and the next step moves the parameter
+// by it, so that two evaluations whose roundings differ would part; m and s are
+// therefore formed by exactly the operations that adamw.h names, each rounded
+// by itself (square root included), and codes and scales come out the same
+// wherever they are formed.
+__device__ __forceinline__ void advance8(float& p, float& m, float ms, float& s, float vs, float g,
+                                         const Ctl& c, const Betas& h) {
+#pragma clang fp contract(off)
+    const float precise = float(fma(h.b1, double(m) * double(ms), h.o1 * (double(g) * c.scale)));
+    g = g * c.factor;
+    m = h.b1f * (m * ms) + h.o1f * g;
+    s = s * vs;
+    s = sqrtf(h.b2 * (s * s) + (h.o2 * g) * g);
+    move(p, precise, s, c, h);
 }
 
 enum { P_, G_, M_, V_, X0_ };  // then: master, and/or the two scales
@@ -292,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void k_step(
             const In<D, BITS8, MASTER>& q = in[u - u0];
             const long long k = at(u);
             const int l = left(u);
-            float pv[kVec], mv[kVec], vv[kVec], sv[kVec];
+            float pv[kVec], mv[kVec], vv[kVec];  // vv: 8 bits, sqrt(v)
             if constexpr (BITS8) {
                 decode(q.cm, mv);
                 decode(q.cv, vv);
@@ -302,18 +331,17 @@ __global__ __launch_bounds__(kThreads) void k_step(
                 if constexpr (MASTER) pv[j] = q.w.get(j);
                 else pv[j] = q.p.get(j);
                 if constexpr (BITS8) {
-                    vv[j] *= q.sv;
-                    vv[j] *= vv[j];
-                    advance(pv[j], mv[j], q.sm, mv[j], vv[j], q.g.get(j), c, h, sv[j]);
+                    advance8(pv[j], mv[j], q.sm, vv[j], q.sv, q.g.get(j), c, h);
                 } else {
+                    mv[j] = q.m.get(j);
                     vv[j] = q.v.get(j);
-                    advance(pv[j], q.m.get(j), 1.f, mv[j], vv[j], q.g.get(j), c, h, sv[j]);
+                    advance(pv[j], mv[j], vv[j], q.g.get(j), c, h);
                 }
             }
             if constexpr (BITS8) {
                 float a, b;
                 put_codes(m + k, encode<false>(mv, uint32_t(k), c.turn, a), l);
-                put_codes(v + k, encode<true>(sv, uint32_t(k), c.turn, b), l);
+                put_codes(v + k, encode<true>(vv, uint32_t(k), c.turn, b), l);
                 if (block(u) * ADAMW_BLOCK < n && threadIdx.x % 64 == 0) {
                     ms[block(u)] = a;
                     vs[block(u)] = b;
@@ -480,7 +508,7 @@ hipError_t step(const adamw_config& c, const adamw_tensor* t, int count, int* st
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const Betas h{c.beta1, 1.0 - c.beta1, float(c.beta2), float(1.0 - c.beta2),
-                  float(c.eps)};
+                  float(c.eps), float(c.beta1), float(1.0 - c.beta1)};
     bool master = false;
     for (int i = 0; i < count && !master; ++i) master = t[i].n > 0 && t[i].w;
     if (c.dtype == ADAMW_F32) return run_type<F32>(c.bits == 8, master, t, count, ctl, h, st);

@@ -12,6 +12,7 @@ namespace adw {
 // What the kernels of one step share, formed on the device by the first of them.
 struct Ctl {
     double scale;  // of the gradients, clipping included
+    float factor;  // the same in fp32 operations, for what is held in 8 bits
     float keep;    // 1 - lr * weight_decay
     float rate;    // lr / (1 - beta1^t)
     float root;    // 1 / sqrt(1 - beta2^t)

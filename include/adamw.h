@@ -17,12 +17,25 @@
  * bits = 32: m and v are fp32.  bits = 8: m and s = sqrt(v) are held as e4m3
  * codes (the OCP format with 448 as its largest value) with one fp32 scale for
  * each ADAMW_BLOCK consecutive elements of a tensor, the last block shorter;
- * value = code * scale.  The update uses the new m and v before they are
- * rounded.  scale is the block's largest magnitude / 448.  A magnitude x
- * (after division by the scale) is rounded down to a code if the fraction of
- * the step to the next code that it has covered, plus a dither d in [0, 1),
- * stays below 1, else up; so its mean over the steps is x, and moments move
- * that change by less than half a step at a time.  No generator is involved:
+ * value = code * scale.  The update uses the new m and v before they are held.
+ *
+ * A code depends on the last bit of what it is formed from, so with bits = 8
+ * codes and scales are defined to that bit.  Each operation below is in fp32 and
+ * rounded to nearest even by itself, each coefficient is the fp32 nearest to its
+ * value, and g is the gradient as stored:
+ *
+ *   f = grad_scale * min(1, max_norm / (norm + 1e-6))   (grad_scale without clipping)
+ *   g = g f    m = beta1 (code scale) + (1 - beta1) g
+ *   r = code scale    s = sqrt(beta2 (r r) + ((1 - beta2) g) g)
+ *   scale = T (1/448)    x = |value| (1 / scale)        (T: the block's largest |value|)
+ *   u = x's step to the next code, a power of two       code = floor(x / u + d) u, at most 448
+ *
+ * That is, x is rounded down to a code if the fraction of the step to the next
+ * code that it has covered, plus a dither d in [0, 1), stays below 1, else up; so
+ * its mean over the steps is x, and moments move that change by less than half a
+ * step at a time.  This holds for T too, whose x is 448 or, by the roundings of
+ * its scale, up to two units in the last place less: then a d below 2^-20 takes
+ * it to 416.  No generator is involved:
  *
  *   d = (((k * 2654435769 + t * 3242174889 + turn) mod 2^32) >> 8) / 2^24
  *
@@ -30,8 +43,9 @@
  * (multiples of the golden ratio and of the inverse plastic number, whose
  * sequences fill the unit interval evenly).  An s that is not 0 takes the
  * lowest code rather than 0, so that no element divides by eps alone.  Blocks
- * whose largest magnitude is below 448 * 2^-126 are held as zeros.  A moment
- * that is not finite is held as NaN and leaves the rest of its block alone.
+ * whose scale is below 2^-126 are held as zeros.  A moment that is not finite is
+ * held as NaN and leaves the rest of its block alone.  The parameter moves by m
+ * and s to fp32 accuracy, as with bits = 32; its last bits are not defined.
  *
  * Ownership, threading, streams and error codes are those of wtconv.h.  The
  * tensor lists are host arrays and are read before the call returns; any
