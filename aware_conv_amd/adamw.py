@@ -30,6 +30,12 @@ def _dtype_code(dtype):
 _PARAM, _GRAD, _MASTER, _M, _V, _M_SCALE, _V_SCALE, _COUNT = range(8)  # columns of the table
 
 
+def _held(ts):
+    """The tensors as a list or tuple.  The table takes their addresses alone: who fills it keeps
+    this until the call was enqueued, or tensors that only an iterator made would be gone."""
+    return ts if isinstance(ts, (list, tuple)) else list(ts)
+
+
 def _column(table, column, name, ts, dtype, device, block=1):
     """The list's addresses into the table, after checking that its tensors are of `dtype`, on
     `device`, contiguous, and of ceil(n / block) elements for the n of the table's last column
@@ -87,7 +93,7 @@ def _workspace(table, device, workspace):
 @on_stream
 def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, *, stream=None):
     """2-norm of ``grad_scale`` times all gradients together, as one fp32 on the device."""
-    grads = list(grads)
+    grads = _held(grads)
     if not grads:
         raise ValueError("adamw_grad_norm needs at least one gradient")
     device = _gpu_of("grads", grads)
@@ -118,9 +124,12 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     fp32 tensors, where the moments are e4m3 codes (exp_avg_sqs of sqrt(v)); without it they are
     fp32.  grad_norm: what adamw_grad_norm gave, for max_norm, and to leave out a step whose norm
     is not finite.  lr and grad_scale may be one-element fp32 tensors on the device."""
-    params = list(params)
+    params = _held(params)
     if not params:
         return
+    grads, exp_avgs, exp_avg_sqs = _held(grads), _held(exp_avgs), _held(exp_avg_sqs)
+    masters = None if masters is None else _held(masters)
+    scales = None if scales is None else [_held(ts) for ts in scales]
     device = _gpu_of("params", params)
     dtype, code = params[0].dtype, _dtype_code(params[0].dtype)
     table = _new_table(len(params))

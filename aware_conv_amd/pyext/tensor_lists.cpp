@@ -21,9 +21,11 @@ enum { OK, COUNT, NOT_TENSOR, DTYPE, DEVICE, LAYOUT, SIZE };
 
 // column(tensors, table, rows, column, dtype, device, block) -> (code, index)
 //
-// tensors: a list or tuple.  table: address of `rows` rows.  column: where the
-// addresses go.  block: 0 writes the numbers of elements to the last column;
-// k > 0 expects ceil(n / k) elements for the n found there.
+// tensors: a list or tuple, which the caller keeps as long as the table is
+// used (nothing else is taken: an iterator's tensors would be gone with it).
+// table: address of `rows` rows.  column: where the addresses go.  block: 0
+// writes the numbers of elements to the last column; k > 0 expects
+// ceil(n / k) elements for the n found there.
 PyObject* column(PyObject*, PyObject* args) {
     PyObject *list, *dtype;
     unsigned long long table;
@@ -37,12 +39,14 @@ PyObject* column(PyObject*, PyObject* args) {
         return nullptr;
     }
     const at::ScalarType type = reinterpret_cast<THPDtype*>(dtype)->scalar_type;
-    PyObject* seq = PySequence_Fast(list, "expected a list of tensors");
-    if (!seq) return nullptr;
-    int code = PySequence_Fast_GET_SIZE(seq) == rows ? OK : COUNT;
+    if (!PyList_Check(list) && !PyTuple_Check(list)) {
+        PyErr_SetString(PyExc_TypeError, "expected a list or tuple of tensors");
+        return nullptr;
+    }
+    int code = PySequence_Fast_GET_SIZE(list) == rows ? OK : COUNT;
     Py_ssize_t i = 0;
     if (code == OK) {
-        PyObject** items = PySequence_Fast_ITEMS(seq);
+        PyObject** items = PySequence_Fast_ITEMS(list);
         long long* row = reinterpret_cast<long long*>(table);
         for (; i < rows; ++i, row += kColumns) {
             if (!THPVariable_Check(items[i])) {
@@ -64,7 +68,6 @@ PyObject* column(PyObject*, PyObject* args) {
             row[col] = reinterpret_cast<long long>(t.data_ptr());
         }
     }
-    Py_DECREF(seq);
     return Py_BuildValue("in", code, i);
 }
 

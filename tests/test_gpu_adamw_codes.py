@@ -175,3 +175,19 @@ def test_two_steps_agree_with_the_plain_form(dtype, master):
     near = (top - out[1]["w" if master else "p"].float()).abs()
     half = 0 if master or dtype == "f32" else 2.0 ** -11
     assert (near <= 1e-6 + 2 * half * top.abs()).all()
+
+
+def test_tensors_that_only_an_iterator_makes():
+    """Gradients converted on the way into the call, against the same in a list."""
+    import aware_conv_amd as A
+    out = []
+    for make_list in (True, False):
+        g = torch.Generator(device="cuda").manual_seed(1)
+        p = [torch.randn(5000 + k, generator=g, device="cuda") for k in range(20)]
+        half = [torch.randn(5000 + k, generator=g, device="cuda").half() for k in range(20)]
+        m, v = ([torch.zeros_like(t) for t in p] for _ in range(2))
+        grads = (t.float() for t in half)
+        step = torch.zeros(1, dtype=torch.int32, device="cuda")
+        A.adamw_step(p, list(grads) if make_list else grads, m, v, step, **HYPER)
+        out.append(p + m + v)
+    assert all(torch.equal(a, b) for a, b in zip(*out))
