@@ -9,12 +9,30 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/util/Exception.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
 
 constexpr int kColumns = 8;  // of a row, 64 bits each: seven addresses, then the number of elements
+
+// A method whose C++ exceptions become Python's.  Asking a tensor for its memory
+// throws where it has none of its own, as inside torch's function transforms; past
+// the interpreter's frames, which are C, an exception would end the process.
+template <PyObject* (*body)(PyObject*)>
+PyObject* guarded(PyObject*, PyObject* args) {
+    try {
+        return body(args);
+    } catch (const c10::Error& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+    }
+    return nullptr;
+}
 
 // What is wrong with a list, for the caller to put into words.
 enum { OK, COUNT, NOT_TENSOR, DTYPE, DEVICE, LAYOUT, SIZE };
@@ -26,7 +44,7 @@ enum { OK, COUNT, NOT_TENSOR, DTYPE, DEVICE, LAYOUT, SIZE };
 // table: address of `rows` rows.  column: where the addresses go.  block: 0
 // writes the numbers of elements to the last column; k > 0 expects
 // ceil(n / k) elements for the n found there.
-PyObject* column(PyObject*, PyObject* args) {
+PyObject* column(PyObject* args) {
     PyObject *list, *dtype;
     unsigned long long table;
     Py_ssize_t rows;
@@ -85,7 +103,7 @@ bool adjacent(const at::Tensor& t) {
 // are None or of its shape, dtype and device, and all have adjacent rows.
 // Writes (pointer, stride of axis 0, stride of axis 1) of each, 64 bits each;
 // zeros for None.
-PyObject* views(PyObject*, PyObject* args) {
+PyObject* views(PyObject* args) {
     PyObject* tuple;
     unsigned long long address;
     if (!PyArg_ParseTuple(args, "O!K", &PyTuple_Type, &tuple, &address)) return nullptr;
@@ -115,7 +133,7 @@ PyObject* views(PyObject*, PyObject* args) {
 // flat(tensor, dtype, device, n0, n1) -> address, None for None, False if it
 // does not fit: contiguous, of that dtype on that CUDA device, of the shape
 // (n0, n1), or (n0,) for a negative n1.
-PyObject* flat(PyObject*, PyObject* args) {
+PyObject* flat(PyObject* args) {
     PyObject *o, *dtype;
     int device;
     long long n0, n1;
@@ -131,9 +149,9 @@ PyObject* flat(PyObject*, PyObject* args) {
     return PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.data_ptr()));
 }
 
-PyMethodDef methods[] = {{"views", views, METH_VARARGS, "Checks strided activations and writes their views."},
-                         {"flat", flat, METH_VARARGS, "Checks a contiguous tensor and returns its address."},
-                         {"column", column, METH_VARARGS, "Checks a list of tensors and writes their addresses."},
+PyMethodDef methods[] = {{"views", guarded<views>, METH_VARARGS, "Checks strided activations and writes their views."},
+                         {"flat", guarded<flat>, METH_VARARGS, "Checks a contiguous tensor and returns its address."},
+                         {"column", guarded<column>, METH_VARARGS, "Checks a list of tensors and writes their addresses."},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
