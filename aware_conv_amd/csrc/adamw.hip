@@ -198,7 +198,7 @@ __global__ void k_begin(int* step, const float* lr_dev, const float* scale_dev, 
             c.factor *= fminf(1.f, float(max_norm) / (n + 1e-6f));
         }
     }
-    c.keep = float(1.0 - lr * decay);
+    c.drop = float(lr * decay);
     c.rate = float(lr / (1.0 - pow(beta1, double(t))));
     c.root = float(1.0 / sqrt(1.0 - pow(beta2, double(t))));
     c.scale = scale;
@@ -216,9 +216,10 @@ struct Betas {
 // The two terms of m may cancel, which would leave an fp32 sum with few of its
 // digits for a parameter whose v is small: the m that moves the parameter is
 // formed in fp64, whose few instructions hide behind the memory accesses, and
-// rounded once.
+// rounded once.  What the parameter changes by is formed before it is added: 1 -
+// lr * decay would keep few digits of a small decay, or none.
 __device__ __forceinline__ void move(float& p, float m, float s, const Ctl& c, const Betas& h) {
-    p = fmaf(p, c.keep, -c.rate * m * gsc::rcp_hw(fmaf(s, c.root, h.eps)));
+    p += fmaf(-c.drop, p, -c.rate * m * gsc::rcp_hw(fmaf(s, c.root, h.eps)));
 }
 
 // New moments and parameter of one element.

@@ -13,7 +13,7 @@ namespace adw {
 struct Ctl {
     double scale;  // of the gradients, clipping included
     float factor;  // the same in fp32 operations, for what is held in 8 bits
-    float keep;    // 1 - lr * weight_decay
+    float drop;    // lr * weight_decay
     float rate;    // lr / (1 - beta1^t)
     float root;    // 1 / sqrt(1 - beta2^t)
     unsigned turn;  // t's part of the dither

@@ -1,0 +1,42 @@
+"""The AdamW step where something in it is small."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,bits", [(torch.float32, 32), (torch.float32, 8), (torch.bfloat16, 32)])
+@pytest.mark.parametrize("lr", [1e-5, 1e-6])
+def test_slow_weight_decay(lr, dtype, bits):
+    """lr * weight_decay of 1e-7 and 1e-8, at and below the spacing of fp32 under 1: with and
+    without it, a million parameters differ on the mean by what 50 steps take off.  Each step
+    rounds a parameter of 0.1 to 0.2 by at most 7.5e-9, evenly, as its update is spread over many
+    units: 4e-9 * sqrt(2 * 50) / 1024 = 4e-11 of noise on the mean, 6e-5 and 6e-4 of the 7.5e-7
+    and 7.5e-8 that are taken off; ten times that is allowed."""
+    import aware_conv_amd as A
+    print("\ncase decay %s" % ((lr, dtype, bits),), flush=True)
+    n, steps, decay = 1 << 20, 50, 0.01
+    ends, path = [], []
+    for wd in (decay, 0.0):
+        g = torch.Generator(device="cuda").manual_seed(1)
+        w = 0.1 + 0.1 * torch.rand(n, generator=g, device="cuda")
+        masters = None if dtype == torch.float32 else [w]
+        p = w if masters is None else w.to(dtype)
+        if bits == 8:
+            codes = torch.randint(48, 120, (2, n), generator=g, device="cuda", dtype=torch.uint8)
+            m, v = (c.view(torch.float8_e4m3fn) for c in codes)
+            scales = [torch.full((n // 256,), 1e-5, device="cuda")], [torch.full((n // 256,), 1e-5, device="cuda")]
+        else:
+            m = torch.randn(n, generator=g, device="cuda") * 1e-3
+            v = 1e-6 * (0.5 + torch.rand(n, generator=g, device="cuda"))
+            scales = None
+        step = torch.full((1,), 100, dtype=torch.int32, device="cuda")
+        for _ in range(steps):
+            path.append(float(w.double().mean()))  # which the updates move, too
+            grad = (torch.randn(n, generator=g, device="cuda") * 1e-3).to(dtype)
+            A.adamw_step([p], [grad], [m], [v], step, lr=lr, weight_decay=wd, masters=masters, scales=scales)
+        ends.append(w.double())
+    # the moments do not depend on the parameters: the updates are the same
+    want = -lr * decay * sum(path[:steps])
+    got = float((ends[0] - ends[1]).mean())
+    assert abs(got / want - 1) <= 6e-9 / lr
