@@ -229,7 +229,10 @@ __device__ __forceinline__ void advance(float& p, float& m, float& v, float g, c
     m = float(fma(h.b1, double(m), h.o1 * gd));
     g = float(gd);
     v = fmaf(h.b2, v, (h.o2 * g) * g);
-    move(p, m, gsc::sqrt_hw(v), c, h);
+    // the library's root: the hardware's instruction takes v below 2^-126 (gradients
+    // below 1e-18 or so) for 0, by which the parameter would be divided where eps is
+    // 0; the rest of its instructions hide behind the memory accesses, too
+    move(p, m, sqrtf(v), c, h);
 }
 
 // The same with moments in 8 bits: m and s are the values of the codes, then

@@ -40,3 +40,24 @@ def test_slow_weight_decay(lr, dtype, bits):
     want = -lr * decay * sum(path[:steps])
     got = float((ends[0] - ends[1]).mean())
     assert abs(got / want - 1) <= 6e-9 / lr
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("size", [1e-16, 1e-17, 1e-18, 1e-19, 1e-20])
+def test_gradients_whose_squares_leave_the_normal_range(size, bits):
+    """Without eps the first step moves a parameter by lr, whatever the gradient: v is exact to
+    1e-6 of itself and 2^-149 (its spacing below 2^-126, two roundings), and its root to half."""
+    import aware_conv_amd as A
+    print("\ncase tiny %s" % ((size, bits),), flush=True)
+    n = 300
+    p = torch.zeros(n, device="cuda")
+    g = torch.full((n,), size, device="cuda")
+    if bits == 8:
+        m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+        scales = [torch.zeros(2, device="cuda")], [torch.zeros(2, device="cuda")]
+    else:
+        m, v, scales = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), None
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    A.adamw_step([p], [g], [m], [v], step, lr=1e-3, eps=0.0, weight_decay=0.0, scales=scales)
+    bound = 1e-3 * (2e-6 + 2.0 ** -150 / (1e-3 * size ** 2))
+    assert ((p.double() + 1e-3).abs() <= bound).all()
