@@ -30,6 +30,8 @@ constexpr int kVec = 4;                           // elements of a lane and acce
 constexpr int kUnits = 4;                         // accesses of a lane
 constexpr int kChunk = kThreads * kVec * kUnits;  // elements of a workgroup
 
+constexpr float kMax = 3.402823466e38f;  // the largest finite value
+
 // P pointers for each of up to N tensors, and the chunks before each.
 template <int P, int N>
 struct Table {
@@ -143,12 +145,12 @@ __device__ __forceinline__ float code_of(float x, float d) {
     const float ulp = __uint_as_float(e - (3u << 23));
     const float per = __uint_as_float((254u << 23) - (e - (3u << 23)));  // 1 / ulp
     const float q = fminf(floorf(fmaf(x, per, d)) * ulp, 448.f);
-    return x <= 3e38f ? q : __uint_as_float(0x7fc00000u);
+    return x <= kMax ? q : __uint_as_float(0x7fc00000u);
 }
 
 __device__ __forceinline__ float finite_abs(float v) {
     const float a = fabsf(v);
-    return a <= 3e38f ? a : 0.f;
+    return a <= kMax ? a : 0.f;
 }
 
 // Codes and scale of a block of the wavefront (four elements per lane): 256
@@ -192,7 +194,7 @@ __global__ void k_begin(int* step, const float* lr_dev, const float* scale_dev, 
     c.factor = float(scale);
     if (norm) {
         const float n = *norm;
-        c.on = fabsf(n) <= 3.4028235e38f;
+        c.on = fabsf(n) <= kMax;
         if (max_norm > 0) {
             scale *= fmin(1.0, max_norm / (double(n) + 1e-6));
             c.factor *= fminf(1.f, float(max_norm) / (n + 1e-6f));

@@ -61,3 +61,21 @@ def test_gradients_whose_squares_leave_the_normal_range(size, bits):
     A.adamw_step([p], [g], [m], [v], step, lr=1e-3, eps=0.0, weight_decay=0.0, scales=scales)
     bound = 1e-3 * (2e-6 + 2.0 ** -150 / (1e-3 * size ** 2))
     assert ((p.double() + 1e-3).abs() <= bound).all()
+
+
+def test_moments_near_the_largest_float():
+    """3.3e38 is finite: it is the largest of its block, and sets its scale.  Codes are exact: the
+    scale is 3.3e38 / 448 to fp32, and every other magnitude of the block is 0 of it."""
+    import aware_conv_amd as A
+    g = torch.ones(256, device="cuda")
+    g[7], g[9] = -3.3e38, float("inf")
+    m, v = (torch.zeros(256, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    scales = [torch.zeros(1, device="cuda")], [torch.zeros(1, device="cuda")]
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    A.adamw_step([torch.zeros(256, device="cuda")], [g], [m], [v], step, betas=(0.0, 0.999), scales=scales)
+    assert abs(float(scales[0][0]) / (3.3e38 / 448) - 1) <= 2.0 ** -23
+    got = m.float().cpu()
+    assert got[7] == -448 and got[9].isnan()
+    got[7] = got[9] = 0
+    # 1 of a scale of 7e35 is 0 or, for a dither that rounds it up, the lowest code
+    assert ((got == 0) | (got == 2.0 ** -9)).all()
