@@ -101,6 +101,7 @@ def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, *, stream=
     table = _new_table(len(grads))
     _column(table, _GRAD, "grads", grads, grads[0].dtype, device, 0)
     scale, scale_dev = _scalar("grad_scale", grad_scale, device)
+    given = norm
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=device)
     else:
@@ -110,6 +111,7 @@ def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, *, stream=
     _lib._check(_lib.lib.adamw_grad_norm(code, table.ctypes.data, len(table), scale, p(scale_dev),
                                          p(norm), p(ws), nws, _raw_stream(stream, device)),
                 "adamw_grad_norm")
+    _lists.written(given)
     return norm
 
 
@@ -161,6 +163,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
                               p(grad_norm))
     _lib._check(_lib.lib.adamw_step(ctypes.byref(config), table.ctypes.data, len(table), p(step),
                                     p(ws), nws, _raw_stream(stream, device)), "adamw_step")
+    _lists.written(params, exp_avgs, exp_avg_sqs, masters, step, *(scales or ()))
 
 
 class AdamW(torch.optim.Optimizer):

@@ -186,6 +186,7 @@ def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, 
     p, (plam, ph0, plen) = _read(v, ("x", "r", "i", "h"), (x, r, i, h),
                                  (("lam", lam, _f32, C, -1), ("h0", h0, _f32, B, C),
                                   ("lengths", lengths, _i32, B, -1)))
+    given = h
     if h is None:
         h = torch.empty(x.shape, dtype=dt, device=dev)
         v[3] = _view(h)
@@ -198,6 +199,8 @@ def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, 
     _lib._check(_lib.lib.gscan_fwd(ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, ph0, plen,
                                    p + 3 * _VIEW, h_last.data_ptr(), pstates, pws, nws,
                                    _raw_stream(stream, dev)), "gscan_fwd")
+    if given is not None:
+        _lists.written(given)
     return h, h_last, states
 
 
@@ -207,6 +210,7 @@ def gscan_bwd(x, r, i, lam, states, dh, dh_last=None, lengths=None, layout="bct"
     """Gradients of <dh, h> + <dh_last, h_last> as a dict keyed by GRAD_NAMES, from the inputs
     and the states of gscan_fwd.  ``grads`` may hold tensors to write (dx, dr, di with free
     strides); those it lacks are allocated."""
+    given = tuple((grads or {}).values())
     grads = dict(grads or {})
     unknown = [n for n in grads if n not in GRAD_NAMES]
     if unknown:
@@ -238,6 +242,7 @@ def gscan_bwd(x, r, i, lam, states, dh, dh_last=None, lengths=None, layout="bct"
     _lib._check(_lib.lib.gscan_bwd(ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, pst, plen,
                                    p + 3 * _VIEW, plast, p + 4 * _VIEW, p + 5 * _VIEW, p + 6 * _VIEW,
                                    pdlam, pdh0, pws, nws, _raw_stream(stream, dev)), "gscan_bwd")
+    _lists.written(given)
     return grads
 
 
@@ -261,11 +266,13 @@ def gscan_step(x, r, i, lam, state, slots=None, decay=8.0, h=None, *, stream=Non
     p, (plam, pstate, pslots) = _read(v, ("x", "r", "i", "h"), (x, r, i, h),
                                       (("lam", lam, _f32, C, -1), ("state", state, _f32, S, C),
                                        ("slots", slots, _i32, B, -1)))
+    given = h
     if h is None:
         h = torch.empty((B, C), dtype=dt, device=dev)
         v[3] = _view(h)
     _lib._check(_lib.lib.gscan_step(B, C, S, code, decay, p, p + _VIEW, p + 2 * _VIEW, plam, pstate,
                                     pslots, p + 3 * _VIEW, _raw_stream(stream, dev)), "gscan_step")
+    _lists.written(state, given)
     return h
 
 

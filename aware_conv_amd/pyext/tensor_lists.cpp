@@ -1,6 +1,6 @@
 // Python extension of the bindings in aware_conv_amd/adamw.py and gscan.py:
 // checks tensors and reads what the library takes of them, in one call for
-// several tensors.  What is wrong is put into words by the caller.
+// several tensors, and tells autograd of those that were written.  What is wrong is put into words by the caller.
 //
 // A step over a hundred small tensors has several hundred of them to check and
 // look up; attribute by attribute from Python that takes longer than the step
@@ -149,9 +149,30 @@ PyObject* flat(PyObject* args) {
     return PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.data_ptr()));
 }
 
+// written(tensors...) -- advances the version counters of what a call has
+// written through its addresses, so that autograd sees a change of what it
+// saved.  Each argument: a tensor, None, or a list or tuple of tensors.
+PyObject* written(PyObject* args) {
+    auto bump = [](PyObject* o) {
+        if (!THPVariable_Check(o)) return;
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();  // those have no counter
+    };
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(args); ++i) {
+        PyObject* o = PyTuple_GET_ITEM(args, i);
+        if (!PyList_Check(o) && !PyTuple_Check(o)) {
+            bump(o);
+            continue;
+        }
+        for (Py_ssize_t k = 0; k < PySequence_Fast_GET_SIZE(o); ++k) bump(PySequence_Fast_GET_ITEM(o, k));
+    }
+    Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {{"views", guarded<views>, METH_VARARGS, "Checks strided activations and writes their views."},
                          {"flat", guarded<flat>, METH_VARARGS, "Checks a contiguous tensor and returns its address."},
                          {"column", guarded<column>, METH_VARARGS, "Checks a list of tensors and writes their addresses."},
+                         {"written", guarded<written>, METH_VARARGS, "Advances tensors' version counters."},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -20,6 +20,9 @@ class Recorder:
         self.seen += [weakref.ref(t) for t in ts]
         return 0, len(ts)
 
+    def written(self, *_):
+        pass
+
     def enqueue(self, *_):
         self.alive = [r() is not None for r in self.seen]
         return 0
@@ -51,3 +54,11 @@ def test_the_extension_takes_no_iterator():
     for ts in ((x for x in [torch.zeros(3)]), {0: torch.zeros(3)}, torch.zeros(1, 3), "a", None):
         with pytest.raises(TypeError, match="list or tuple"):
             gscan._lists.column(ts, t.ctypes.data, 1, 0, torch.float32, 0, 0)
+
+
+def test_written_tensors_have_new_versions():
+    a, b, c, d = (torch.zeros(2) for _ in range(4))
+    with torch.inference_mode():
+        e = torch.zeros(2)
+    gscan._lists.written(a, None, [b, c], (), (d, e), e)
+    assert [t._version for t in (a, b, c, d)] == [1, 1, 1, 1]
