@@ -176,6 +176,8 @@ class AdamW(torch.optim.Optimizer):
     steps whose norm is not finite, moments and step numbers included.  lr (of a group) and
     grad_scale (an attribute: 1 / the loss scale) may be fp32 tensors on the device."""
 
+    _OPTIONS = ("bits", "master", "max_norm", "skip_nonfinite", "grad_scale")
+
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32,
                  master=True, max_norm=None, skip_nonfinite=False, grad_scale=1.0):
         if bits not in (8, 32):
@@ -187,6 +189,9 @@ class AdamW(torch.optim.Optimizer):
         self.bits, self.master, self.max_norm = bits, master, max_norm
         self.skip_nonfinite, self.grad_scale = skip_nonfinite, grad_scale
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+
+    def __getstate__(self):  # of copies and pickles; the base class keeps its own attributes alone
+        return dict(super().__getstate__(), **{n: getattr(self, n) for n in self._OPTIONS})
 
     def _new_state(self, p, step):
         if not p.is_contiguous():

@@ -191,3 +191,29 @@ def test_tensors_that_only_an_iterator_makes():
         A.adamw_step(p, list(grads) if make_list else grads, m, v, step, **HYPER)
         out.append(p + m + v)
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_copied_optimizer_goes_on_as_the_first(bits):
+    import copy
+    import aware_conv_amd as A
+    p = [torch.nn.Parameter(torch.randn(n, generator=torch.Generator().manual_seed(n)).half().cuda())
+         for n in (300, 5)]
+    opt = A.AdamW(p, bits=bits, max_norm=0.1, grad_scale=0.5, **HYPER)
+
+    def steps(p, opt, seed):
+        for t in range(2):
+            for k, w in enumerate(p):
+                g = torch.Generator().manual_seed(100 * seed + 10 * t + k)
+                w.grad = torch.randn(w.shape, generator=g).half().cuda()
+            opt.step()
+
+    steps(p, opt, 1)
+    p2, opt2 = copy.deepcopy((p, opt))
+    steps(p, opt, 2)
+    steps(p2, opt2, 2)
+    for a, b in zip(p, p2):
+        assert torch.equal(a, b)
+        for n, t in opt.state[a].items():
+            assert torch.equal(t.view(torch.uint8), opt2.state[b][n].view(torch.uint8)), n
+    assert opt2.state[p2[0]]["step"] is opt2.state[p2[1]]["step"]
