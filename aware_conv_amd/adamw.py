@@ -7,6 +7,7 @@ given as tensors, the learning rate and the gradient scale stay on the device:
 a step neither synchronises nor copies, and can be captured into a graph.
 """
 import ctypes
+import math
 
 import numpy as np
 import torch
@@ -192,6 +193,13 @@ class AdamW(torch.optim.Optimizer):
 
     def __getstate__(self):  # of copies and pickles; the base class keeps its own attributes alone
         return dict(super().__getstate__(), **{n: getattr(self, n) for n in self._OPTIONS})
+
+    def add_param_group(self, param_group):
+        for n in ("lr", "eps", "weight_decay"):
+            v = param_group.get(n, self.defaults[n])
+            if not isinstance(v, torch.Tensor) and not 0.0 <= v < math.inf:
+                raise ValueError("%s must be finite and not negative, got %r" % (n, v))
+        super().add_param_group(param_group)
 
     def _new_state(self, p, step):
         if not p.is_contiguous():

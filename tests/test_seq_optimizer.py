@@ -27,3 +27,18 @@ def test_copies_have_the_options(copied):
         assert getattr(other, n) == v, n
     assert other.param_groups[0]["lr"] == 0.1
     assert other.step() is None  # nothing has a gradient
+
+
+@pytest.mark.parametrize("kw", [{"lr": -1e-3}, {"eps": -1e-8}, {"weight_decay": -0.1}, {"lr": float("nan")},
+                                {"eps": float("nan")}, {"weight_decay": float("inf")}, {"lr": float("inf")}])
+def test_values_that_mean_nothing(kw):
+    w = torch.nn.Parameter(torch.zeros(3))
+    with pytest.raises(ValueError, match=list(kw)[0]):
+        AdamW([w], **kw)
+    with pytest.raises(ValueError, match=list(kw)[0]):
+        AdamW([dict(params=[w], **kw)])
+    opt = AdamW([torch.nn.Parameter(torch.zeros(2))])
+    with pytest.raises(ValueError, match=list(kw)[0]):
+        opt.add_param_group(dict(params=[w], **kw))
+    assert len(opt.param_groups) == 1
+    AdamW([w], lr=torch.tensor(-1.0))  # a device value is not looked at
