@@ -175,7 +175,9 @@ class AdamW(torch.optim.Optimizer):
     bits: 32 or 8, of the moments.  master: keep fp32 copies of 16-bit parameters.  max_norm:
     clip the norm of all gradients together.  skip_nonfinite (implied by max_norm): leave out
     steps whose norm is not finite, moments and step numbers included.  lr (of a group) and
-    grad_scale (an attribute: 1 / the loss scale) may be fp32 tensors on the device."""
+    grad_scale (an attribute: 1 / the loss scale) may be fp32 tensors on the device.
+
+    Parameters are contiguous and, where steps are clipped or left out, all on one device."""
 
     _OPTIONS = ("bits", "master", "max_norm", "skip_nonfinite", "grad_scale")
 
@@ -200,6 +202,9 @@ class AdamW(torch.optim.Optimizer):
             if not isinstance(v, torch.Tensor) and not 0.0 <= v < math.inf:
                 raise ValueError("%s must be finite and not negative, got %r" % (n, v))
         super().add_param_group(param_group)
+        if not all(p.is_contiguous() for p in self.param_groups[-1]["params"]):
+            self.param_groups.pop()
+            raise ValueError("parameters must be contiguous")
 
     def _new_state(self, p, step):
         if not p.is_contiguous():

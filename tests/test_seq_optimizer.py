@@ -42,3 +42,9 @@ def test_values_that_mean_nothing(kw):
         opt.add_param_group(dict(params=[w], **kw))
     assert len(opt.param_groups) == 1
     AdamW([w], lr=torch.tensor(-1.0))  # a device value is not looked at
+
+
+def test_strided_parameters_are_refused_when_they_are_given():
+    w = torch.nn.Parameter(torch.zeros(2, 3, 4, 4).to(memory_format=torch.channels_last))
+    with pytest.raises(ValueError, match="contiguous"):
+        AdamW([w])
