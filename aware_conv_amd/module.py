@@ -78,6 +78,16 @@ class GatedScan2d(torch.nn.Module):
         self.lam = torch.nn.Parameter(lam.repeat(2 if both else 1, 1).to(device))
         self.scale = 1 / math.sqrt(2) if both else 1.0
 
+    def _apply(self, fn, recurse=True):
+        """Conversions of the layer (half(), to(dtype), ...) move lam and leave its dtype."""
+        lam = [t for t in (self.lam, self.lam.grad) if t is not None]
+
+        def converted(t):
+            new = fn(t)
+            return t.to(new.device) if any(t is k for k in lam) and new.dtype != t.dtype else new
+
+        return super()._apply(converted, recurse)
+
     def forward(self, x):
         x = x.contiguous()
         r, i = self.reset(x), self.input(x)
