@@ -20,14 +20,18 @@ gsc::Plan plan_of(const gscan_shape& s) {
     return s.layout == GSCAN_BCT ? gsc::planes_plan(s) : gsc::tokens_plan(s);
 }
 
-int check_shape(const gscan_shape* s) {
+int check_form(const gscan_shape* s) {
     if (!s) return WTCONV_ERR_NULL;
     if (s->B < 0 || s->C < 0 || s->T < 0 || s->T > (1 << 30)) return WTCONV_ERR_SHAPE;
     if (s->dtype != GSCAN_F32 && s->dtype != GSCAN_F16 && s->dtype != GSCAN_BF16)
         return WTCONV_ERR_DTYPE;
     if (s->layout != GSCAN_BCT && s->layout != GSCAN_BTC) return WTCONV_ERR_LAYOUT;
     if (!(s->decay > 0.f) || !isfinite(s->decay)) return WTCONV_ERR_VALUE;
-    if ((long long)s->B * s->C > kMaxRows) return WTCONV_ERR_SHAPE;
+    return (long long)s->B * s->C > kMaxRows ? WTCONV_ERR_SHAPE : WTCONV_OK;
+}
+int check_shape(const gscan_shape* s) {
+    const int rc = check_form(s);
+    if (rc) return rc;
     return plan_of(*s).fits ? WTCONV_OK : WTCONV_ERR_UNSUPPORTED;
 }
 
@@ -285,7 +289,7 @@ int gscan_step(int B, int C, int S, int dtype, float decay, const gscan_view* x,
                const gscan_view* r, const gscan_view* i, const float* lam, float* state,
                const int* slots, const gscan_view* h, void* stream) {
     const gscan_shape s{B, C, 1, GSCAN_BTC, dtype, 0, decay};
-    int rc = check_shape(&s);
+    int rc = check_form(&s);  // any number of rows fits its launch
     if (rc) return rc;
     if (S < 0 || (long long)S * C > (1LL << 40)) return WTCONV_ERR_SHAPE;
     if (!slots && S < B) return WTCONV_ERR_SHAPE;

@@ -33,8 +33,9 @@ struct Plan {
     long long parts;  // rows of partial sums of dlam
     size_t states;   // bytes
     size_t scratch;  // bytes of workspace
-    bool fits;       // one launch holds the call's threads (fewer than 2^32)
+    bool fits;       // one launch holds the call's threads
 };
+constexpr long long kMaxThreads = 1LL << 32;  // a launch holds fewer
 
 Plan planes_plan(const gscan_shape& s);
 hipError_t planes_fwd(const gscan_shape& s, Args a, void* ws, hipStream_t st);

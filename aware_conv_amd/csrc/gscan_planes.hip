@@ -632,7 +632,8 @@ Plan planes_plan(const gscan_shape& s) {
     p.parts = f.LW == 0 ? (long long)p.tiles * s.B : s.B;
     p.states = sizeof(float) * size_t(p.tiles) * s.B * s.C;
     p.scratch = words_of(s, f, p.tiles) + sizeof(float) * size_t(p.parts) * s.C;
-    p.fits = f.LW != 0 || (double)s.B * s.C * p.tiles * kSpread < 4e9;
+    // a row that is walked takes a wavefront at the most, of rows fewer than 2^26
+    p.fits = f.LW != 0 || (long long)s.B * s.C * p.tiles < kMaxThreads / kSpread;
     return p;
 }
 

@@ -582,7 +582,11 @@ Plan tokens_plan(const gscan_shape& s) {
     p.parts = (long long)p.tiles * s.B;
     p.states = sizeof(float) * size_t(p.tiles) * s.B * s.C;
     p.scratch = tokens_carry(s, p.tiles) + sizeof(float) * size_t(p.parts) * s.C;
-    p.fits = (double)((s.C + kChan - 1) / kChan) * s.B * p.tiles * kLanes * kFwdSub < 4e9;
+    // forwards a tile has twice the positions and twice the threads; rounded up
+    // to whole tiles, it needs as many threads or more
+    static_assert(kFwdSub == 2 * kBwdSub, "the forward's launch is the larger");
+    const long long units = (long long)((s.C + kChan - 1) / kChan) * s.B;
+    p.fits = units * tiles_of(s.T, kFwdSub * kLen) < kMaxThreads / (kLanes * kFwdSub);
     return p;
 }
 

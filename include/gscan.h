@@ -78,10 +78,12 @@ typedef struct {
 } gscan_view;
 
 /*
- * Sizes: T up to 2^30, B * C up to 2^25 (WTCONV_ERR_SHAPE beyond).  Tokens of
- * fewer than 64 channels, or planes, of so many positions that one launch does
- * not hold their threads (2^31 positions or more in all) are refused with
- * WTCONV_ERR_UNSUPPORTED.
+ * Sizes: T up to 2^30, B * C up to 2^25 (WTCONV_ERR_SHAPE beyond).  What one
+ * launch does not hold is refused with WTCONV_ERR_UNSUPPORTED: tokens unless
+ * ceil(C / 64) * B * ceil(T / 256) is below 2^23 (2^31 positions of up to 64
+ * channels), and planes of up to 1024 rows (B * C) unless B * C *
+ * ceil(T / 4096) is below 2^23 (2^35 positions).  Planes of more rows are
+ * taken, whatever their length, and so are single positions.
  */
 
 /* Bytes of the states gscan_fwd writes for gscan_bwd (what h held before each
