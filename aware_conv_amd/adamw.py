@@ -37,11 +37,11 @@ def _held(ts):
     return ts if isinstance(ts, (list, tuple)) else list(ts)
 
 
-def _column(table, column, name, ts, dtype, device, block=1):
-    """The list's addresses into the table, after checking that its tensors are of `dtype`, on
-    `device`, contiguous, and of ceil(n / block) elements for the n of the table's last column
-    (block 0: of any number, which that column then takes)."""
-    code, k = _lists.column(ts, table.ctypes.data, len(table), column, dtype, device.index, block)
+def _column(table, at, column, name, ts, dtype, device, block=1):
+    """The list's addresses into the table, which lies `at` its own, after checking that its
+    tensors are of `dtype`, on `device`, contiguous, and of ceil(n / block) elements for the n of
+    the table's last column (block 0: of any number, which that column then takes)."""
+    code, k = _lists.column(ts, at, len(table), column, dtype, device.index, block)
     if code == 0:
         return
     if code == 1:
@@ -80,10 +80,10 @@ def _scalar(name, v, device):
     return float(v), None
 
 
-def _workspace(table, device, workspace):
+def _workspace(table, at, device, workspace):
     if workspace is None:
         n = ctypes.c_size_t(0)
-        _lib._check(_lib.lib.adamw_workspace_size(table.ctypes.data, len(table), ctypes.byref(n)),
+        _lib._check(_lib.lib.adamw_workspace_size(at, len(table), ctypes.byref(n)),
                     "adamw_workspace_size")
         workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
     elif not workspace.is_contiguous() or workspace.device != device:
@@ -100,16 +100,17 @@ def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, *, stream=
     device = _gpu_of("grads", grads)
     code = _dtype_code(grads[0].dtype)
     table = _new_table(len(grads))
-    _column(table, _GRAD, "grads", grads, grads[0].dtype, device, 0)
+    at = table.ctypes.data  # asked for once: numpy takes 1 us for it
+    _column(table, at, _GRAD, "grads", grads, grads[0].dtype, device, 0)
     scale, scale_dev = _scalar("grad_scale", grad_scale, device)
     given = norm
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=device)
     else:
         _scalar("norm", norm, device)
-    ws, nws = _workspace(table, device, workspace)
+    ws, nws = _workspace(table, at, device, workspace)
     p = _lib._ptr
-    _lib._check(_lib.lib.adamw_grad_norm(code, table.ctypes.data, len(table), scale, p(scale_dev),
+    _lib._check(_lib.lib.adamw_grad_norm(code, at, len(table), scale, p(scale_dev),
                                          p(norm), p(ws), nws, _raw_stream(stream, device)),
                 "adamw_grad_norm")
     _lists.written(given)
@@ -136,16 +137,17 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     device = _gpu_of("params", params)
     dtype, code = params[0].dtype, _dtype_code(params[0].dtype)
     table = _new_table(len(params))
-    _column(table, _PARAM, "params", params, dtype, device, 0)
-    _column(table, _GRAD, "grads", grads, dtype, device)
+    at = table.ctypes.data
+    _column(table, at, _PARAM, "params", params, dtype, device, 0)
+    _column(table, at, _GRAD, "grads", grads, dtype, device)
     state = CODES if scales is not None else torch.float32
-    _column(table, _M, "exp_avgs", exp_avgs, state, device)
-    _column(table, _V, "exp_avg_sqs", exp_avg_sqs, state, device)
+    _column(table, at, _M, "exp_avgs", exp_avgs, state, device)
+    _column(table, at, _V, "exp_avg_sqs", exp_avg_sqs, state, device)
     if masters is not None:
-        _column(table, _MASTER, "masters", masters, torch.float32, device)
+        _column(table, at, _MASTER, "masters", masters, torch.float32, device)
     if scales is not None:
-        _column(table, _M_SCALE, "scales[0]", scales[0], torch.float32, device, BLOCK)
-        _column(table, _V_SCALE, "scales[1]", scales[1], torch.float32, device, BLOCK)
+        _column(table, at, _M_SCALE, "scales[0]", scales[0], torch.float32, device, BLOCK)
+        _column(table, at, _V_SCALE, "scales[1]", scales[1], torch.float32, device, BLOCK)
     if not isinstance(step, torch.Tensor) or step.dtype != torch.int32 or step.numel() != 1 or \
             step.device != device:
         raise ValueError("step must be one int32 on %s" % device)
@@ -157,12 +159,12 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
         if not isinstance(grad_norm, torch.Tensor):
             raise TypeError("grad_norm must be a torch.Tensor")
         _scalar("grad_norm", grad_norm, device)
-    ws, nws = _workspace(table, device, workspace)
+    ws, nws = _workspace(table, at, device, workspace)
     p = _lib._ptr
     config = _lib.AdamwConfig(code, 8 if scales is not None else 32, lr, betas[0], betas[1], eps,
                               weight_decay, scale, max_norm or 0.0, p(lr_dev), p(scale_dev),
                               p(grad_norm))
-    _lib._check(_lib.lib.adamw_step(ctypes.byref(config), table.ctypes.data, len(table), p(step),
+    _lib._check(_lib.lib.adamw_step(ctypes.byref(config), at, len(table), p(step),
                                     p(ws), nws, _raw_stream(stream, device)), "adamw_step")
     _lists.written(params, exp_avgs, exp_avg_sqs, masters, step, *(scales or ()))
 
