@@ -204,6 +204,17 @@ def _check(rc, where):
         raise WTConvError(rc, where)
 
 
+def _enqueue(device, name, *args):
+    """The library's `name` with the device of its tensors as the current one: it launches on the
+    current device, and a default stream's handle does not name one."""
+    if torch._C._cuda_getDevice() == device.index:
+        rc = getattr(lib, name)(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib, name)(*args)
+    _check(rc, name)
+
+
 def wtconv_workspace_size(shape):
     n = ctypes.c_size_t(0)
     _check(lib.wtconv_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
@@ -227,9 +238,9 @@ def wtconv_fwd(x, w_base, b_base, s_base, w_wav, s_wav, y=None,
     if y is None:
         y = torch.empty_like(x)
     ws, nws = _workspace(s, x.device, workspace)
-    _check(lib.wtconv_fwd(ctypes.byref(s), _ptr(x), _ptr(w_base), _ptr(b_base),
-                          _ptr(s_base), _ptr(w_wav), _ptr(s_wav), _ptr(y),
-                          _ptr(ws), nws, _stream(stream, x.device)), "wtconv_fwd")
+    _enqueue(x.device, "wtconv_fwd", ctypes.byref(s), _ptr(x), _ptr(w_base), _ptr(b_base),
+             _ptr(s_base), _ptr(w_wav), _ptr(s_wav), _ptr(y), _ptr(ws), nws,
+             _stream(stream, x.device))
     return y
 
 
@@ -242,10 +253,8 @@ def wtconv_bwd_input(dy, w_base, s_base, w_wav, s_wav, dx=None,
     if dx is None:
         dx = torch.empty_like(dy)
     ws, nws = _workspace(s, dy.device, workspace)
-    _check(lib.wtconv_bwd_input(ctypes.byref(s), _ptr(dy), _ptr(w_base),
-                                _ptr(s_base), _ptr(w_wav), _ptr(s_wav), _ptr(dx),
-                                _ptr(ws), nws, _stream(stream, dy.device)),
-           "wtconv_bwd_input")
+    _enqueue(dy.device, "wtconv_bwd_input", ctypes.byref(s), _ptr(dy), _ptr(w_base), _ptr(s_base),
+             _ptr(w_wav), _ptr(s_wav), _ptr(dx), _ptr(ws), nws, _stream(stream, dy.device))
     return dx
 
 
@@ -286,10 +295,9 @@ def wtconv_bwd_weight(x, dy, w_base, b_base, s_base, w_wav, s_wav, grads=None,
     if grads is None:
         grads = _grads(w_base, b_base, s_base, w_wav, s_wav)
     ws, nws = _workspace(s, x.device, workspace)
-    _check(lib.wtconv_bwd_weight(
-        ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w_base), _ptr(b_base), _ptr(s_base),
-        _ptr(w_wav), _ptr(s_wav), *[_ptr(grads[n]) for n in GRAD_NAMES],
-        _ptr(ws), nws, _stream(stream, x.device)), "wtconv_bwd_weight")
+    _enqueue(x.device, "wtconv_bwd_weight", ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w_base),
+             _ptr(b_base), _ptr(s_base), _ptr(w_wav), _ptr(s_wav),
+             *[_ptr(grads[n]) for n in GRAD_NAMES], _ptr(ws), nws, _stream(stream, x.device))
     return grads
 
 
@@ -306,10 +314,9 @@ def wtconv_bwd(x, dy, w_base, b_base, s_base, w_wav, s_wav, dx=None, grads=None,
     if grads is None:
         grads = _grads(w_base, b_base, s_base, w_wav, s_wav)
     ws, nws = _workspace(s, x.device, workspace)
-    _check(lib.wtconv_bwd(
-        ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w_base), _ptr(b_base), _ptr(s_base),
-        _ptr(w_wav), _ptr(s_wav), _ptr(dx), *[_ptr(grads[n]) for n in GRAD_NAMES],
-        _ptr(ws), nws, _stream(stream, x.device)), "wtconv_bwd")
+    _enqueue(x.device, "wtconv_bwd", ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w_base),
+             _ptr(b_base), _ptr(s_base), _ptr(w_wav), _ptr(s_wav), _ptr(dx),
+             *[_ptr(grads[n]) for n in GRAD_NAMES], _ptr(ws), nws, _stream(stream, x.device))
     return dx, grads
 
 
@@ -325,10 +332,9 @@ def wtconv_bwd_noalloc(x, dy, w_base, b_base, s_base, w_wav, s_wav, dx, grads,
                 (w_base, b_base, s_base, w_wav, s_wav), None)
     _grads_on_gpu(x, grads)
     s = shape_of(x, w_wav)
-    _check(lib.wtconv_bwd_noalloc(
-        ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w_base), _ptr(b_base), _ptr(s_base),
-        _ptr(w_wav), _ptr(s_wav), _ptr(dx), *[_ptr(grads[n]) for n in GRAD_NAMES],
-        _stream(stream, x.device)), "wtconv_bwd_noalloc")
+    _enqueue(x.device, "wtconv_bwd_noalloc", ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w_base),
+             _ptr(b_base), _ptr(s_base), _ptr(w_wav), _ptr(s_wav), _ptr(dx),
+             *[_ptr(grads[n]) for n in GRAD_NAMES], _stream(stream, x.device))
     return dx, grads
 
 
@@ -367,8 +373,8 @@ def dwconv_fwd(x, w, bias, y=None, stream=None):
     s = dw_shape_of(x, w)
     if y is None:
         y = torch.empty_like(x)
-    _check(lib.dwconv_fwd(ctypes.byref(s), _ptr(x), _ptr(w), _ptr(bias), _ptr(y),
-                          _stream(stream, x.device)), "dwconv_fwd")
+    _enqueue(x.device, "dwconv_fwd", ctypes.byref(s), _ptr(x), _ptr(w), _ptr(bias), _ptr(y),
+             _stream(stream, x.device))
     return y
 
 
@@ -384,7 +390,7 @@ def dwconv_bwd(x, dy, w, dx=None, dw=None, db=None, workspace=None, stream=None)
     need = dwconv_workspace_size(s)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
-    _check(lib.dwconv_bwd(ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w), _ptr(dx), _ptr(dw),
-                          _ptr(db), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                          _stream(stream, x.device)), "dwconv_bwd")
+    _enqueue(x.device, "dwconv_bwd", ctypes.byref(s), _ptr(x), _ptr(dy), _ptr(w), _ptr(dx),
+             _ptr(dw), _ptr(db), _ptr(workspace), workspace.numel() * workspace.element_size(),
+             _stream(stream, x.device))
     return dx, dw, db

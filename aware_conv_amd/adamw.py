@@ -110,9 +110,8 @@ def adamw_grad_norm(grads, grad_scale=1.0, norm=None, workspace=None, *, stream=
         _scalar("norm", norm, device)
     ws, nws = _workspace(table, at, device, workspace)
     p = _lib._ptr
-    _lib._check(_lib.lib.adamw_grad_norm(code, at, len(table), scale, p(scale_dev),
-                                         p(norm), p(ws), nws, _raw_stream(stream, device)),
-                "adamw_grad_norm")
+    _lib._enqueue(device, "adamw_grad_norm", code, at, len(table), scale, p(scale_dev), p(norm),
+                  p(ws), nws, _raw_stream(stream, device))
     _lists.written(given)
     return norm
 
@@ -164,8 +163,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
     config = _lib.AdamwConfig(code, 8 if scales is not None else 32, lr, betas[0], betas[1], eps,
                               weight_decay, scale, max_norm or 0.0, p(lr_dev), p(scale_dev),
                               p(grad_norm))
-    _lib._check(_lib.lib.adamw_step(ctypes.byref(config), at, len(table), p(step),
-                                    p(ws), nws, _raw_stream(stream, device)), "adamw_step")
+    _lib._enqueue(device, "adamw_step", ctypes.byref(config), at, len(table), p(step), p(ws), nws,
+                  _raw_stream(stream, device))
     _lists.written(params, exp_avgs, exp_avg_sqs, masters, step, *(scales or ()))
 
 

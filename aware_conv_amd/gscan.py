@@ -131,9 +131,14 @@ def on_stream(call):
 
 
 def _raw_stream(stream, device):
-    """The stream's handle; without a stream, that of the current one, as an integer (a Stream
-    object would cost as much as the rest of a small call's marshalling)."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    """The handle of a stream, which must be on the tensors' device; without one, that of the
+    device's current stream, as an integer (a Stream object would cost as much as the rest of a
+    small call's marshalling)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError("stream is on %s; every tensor is on %s" % (stream.device, device))
+    return stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=256)
@@ -196,9 +201,8 @@ def gscan_fwd(x, r, i, lam, h0=None, lengths=None, layout="bct", reverse=False, 
         states = torch.empty(_sizes(s.B, s.C, s.T, s.layout, code)[0], dtype=_f32, device=dev)
         pstates = states.data_ptr()
     ws, pws, nws = _workspace(s, dev, workspace)
-    _lib._check(_lib.lib.gscan_fwd(ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, ph0, plen,
-                                   p + 3 * _VIEW, h_last.data_ptr(), pstates, pws, nws,
-                                   _raw_stream(stream, dev)), "gscan_fwd")
+    _lib._enqueue(dev, "gscan_fwd", ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, ph0, plen,
+                  p + 3 * _VIEW, h_last.data_ptr(), pstates, pws, nws, _raw_stream(stream, dev))
     if given is not None:
         _lists.written(given)
     return h, h_last, states
@@ -239,9 +243,9 @@ def gscan_bwd(x, r, i, lam, states, dh, dh_last=None, lengths=None, layout="bct"
         grads["dh0"] = torch.empty((B, C), dtype=_f32, device=dev)
         pdh0 = grads["dh0"].data_ptr()
     ws, pws, nws = _workspace(s, dev, workspace)
-    _lib._check(_lib.lib.gscan_bwd(ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, pst, plen,
-                                   p + 3 * _VIEW, plast, p + 4 * _VIEW, p + 5 * _VIEW, p + 6 * _VIEW,
-                                   pdlam, pdh0, pws, nws, _raw_stream(stream, dev)), "gscan_bwd")
+    _lib._enqueue(dev, "gscan_bwd", ctypes.byref(s), p, p + _VIEW, p + 2 * _VIEW, plam, pst, plen,
+                  p + 3 * _VIEW, plast, p + 4 * _VIEW, p + 5 * _VIEW, p + 6 * _VIEW, pdlam, pdh0,
+                  pws, nws, _raw_stream(stream, dev))
     _lists.written(given)
     return grads
 
@@ -270,8 +274,8 @@ def gscan_step(x, r, i, lam, state, slots=None, decay=8.0, h=None, *, stream=Non
     if h is None:
         h = torch.empty((B, C), dtype=dt, device=dev)
         v[3] = _view(h)
-    _lib._check(_lib.lib.gscan_step(B, C, S, code, decay, p, p + _VIEW, p + 2 * _VIEW, plam, pstate,
-                                    pslots, p + 3 * _VIEW, _raw_stream(stream, dev)), "gscan_step")
+    _lib._enqueue(dev, "gscan_step", B, C, S, code, decay, p, p + _VIEW, p + 2 * _VIEW, plam,
+                  pstate, pslots, p + 3 * _VIEW, _raw_stream(stream, dev))
     _lists.written(state, given)
     return h
 

@@ -34,6 +34,7 @@ def test_tensors_of_any_iterable_live_until_the_step_is_enqueued(monkeypatch, na
     monkeypatch.setattr(adamw, "_lists", rec)
     monkeypatch.setattr(adamw, "_gpu_of", lambda _, ts: ts[0].device)
     monkeypatch.setattr(adamw, "_raw_stream", lambda *_: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: None)  # that of CPU tensors
 
     class Lib:
         adamw_step = rec.enqueue
