@@ -5,9 +5,9 @@
 // nothing is copied or kept, and a captured launch keeps its own); a workgroup
 // takes one chunk of one tensor.  The step is bound by HBM: it reads and
 // writes each value once, 16 bytes per lane and access where the type allows.
-// 94M elements in fp32: 506 us, 5.2 TB/s; 140M in bf16 with masters and 8-bit
-// moments 403 us, 5.6 TB/s (a large copy reaches 4.94 TB/s).  Ninety tensors of
-// 1.06M elements together take 10 us, mostly launch latency.
+// 94M elements in fp32: 504 to 512 us, 5.2 TB/s; 140M in bf16 with masters and
+// 8-bit moments 403 to 416 us, 5.5 TB/s (a large copy reaches 4.94 TB/s).  Ninety
+// tensors of 1.06M elements together take 10 us, mostly launch latency.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -274,7 +274,8 @@ struct In {
 // wait for one another, unit by unit.  94M elements in fp32: 515 us unit by
 // unit, 509 with all four at once; 140M with 8-bit moments and masters 413 unit
 // by unit, 402 in pairs, 402 with four at once (and 18 us in place of 16.5 for
-// 37 small tensors, whose registers four at once double).
+// 37 small tensors, whose registers four at once double).  The rounded operations
+// that adamw.h names made the pairs 403 and 18.6 us.
 template <class D, bool BITS8, bool MASTER>
 __global__ __launch_bounds__(kThreads) void k_step(
     Table<kPtrs<D, BITS8, MASTER>, kFit<kPtrs<D, BITS8, MASTER>>> t, const Ctl* ctl, Betas h) {
@@ -362,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void k_step(
     }
 }
 
-// Partial sums of squares: 140M bf16 elements in 61 us (4.6 TB/s) where they
+// Partial sums of squares: 140M bf16 elements in 63 us (4.4 TB/s) where they
 // come from HBM at a stretch.
 template <class D>
 __global__ __launch_bounds__(kThreads) void k_squares(Table<1, kFit<1>> t, double* part) {

@@ -16,11 +16,11 @@
 // the maps u -> a (dh + u), scanned in the other direction.
 //
 // What bounds it, at the rate a large copy reaches on the same card (4.94
-// TB/s): HBM for whole wavefronts per row -- 128x96x56x56 fp16 77 us forwards
-// (4.0 TB/s), 102 us backwards (5.3 TB/s); 8x64x512x512 fp32, spread, 450 us
-// (4.8 TB/s) and 755 us (5.0 TB/s).  Rows that fill part of a wavefront cost
-// the rest of it: 64x384x14x14 fp32 (49 of 64 lanes) 20 us (3.8 TB/s) and 32 us
-// (4.2 TB/s).  8 positions per lane make two 16-byte accesses per tensor in
+// TB/s): HBM for whole wavefronts per row -- 128x96x56x56 fp16 79 us forwards
+// (3.9 TB/s), 107 to 118 us backwards (4.6 to 5.0 TB/s); 8x64x512x512 fp32,
+// spread, 451 us (4.8 TB/s) and 756 us (5.0 TB/s).  Rows that fill part of a
+// wavefront cost the rest of it: 64x384x14x14 fp32 (49 of 64 lanes) 21 us (3.7
+// TB/s) and 33 us (4.1 TB/s).  8 positions per lane make two 16-byte accesses per tensor in
 // fp32 and one in 16 bits, and amortise the 12 DPP moves of a scan; prefetching
 // the next tile shortened a lone row by a tenth but cost the occupancy that
 // many rows need (fp16 above: the backward call 119 -> 144 us), so it is not done.

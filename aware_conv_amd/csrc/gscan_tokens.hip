@@ -10,16 +10,18 @@
 // once.
 //
 // What bounds it (8x4096x2048, against a large copy's 4.94 TB/s): in fp32 HBM
-// (210 us forwards, 5.1 TB/s; 397 us backwards, 4.7 TB/s); in bf16, with half
-// the bytes for the same arithmetic, the vector ALU is busy for 57% of the
-// forward (132 us, 4.1 TB/s) and 51% of the backward (245 us, 3.8 TB/s) and
-// the rest is the tile's latency chain: counter, loads, LDS, the wait for the
-// tiles before.  16 positions per thread amortise the address and LDS work
-// (8: 145 and 304 us); 8 threads along time backwards hold 32 elements in up
-// to 256 registers, two workgroups to a unit, which beats more threads of
-// fewer registers (512 threads of 16 elements: 304 us).  Wider tiles (128
-// channels) and workgroups that stay and fetch their next unit early were
-// slower (267 and 293 us backwards).
+// (213 us forwards, 5.0 TB/s; 396 us backwards, 4.7 TB/s); in bf16, with half
+// the bytes for the same arithmetic, the vector ALU is busy for 59% of the
+// forward (130 to 145 us, 3.7 to 4.1 TB/s) and 52% of the backward (236 to 255
+// us, 3.7 to 4.0 TB/s) and the rest is the tile's latency chain: counter, loads,
+// LDS, the wait for the tiles before.  16 positions per thread amortise the
+// address and LDS work (8: 145 and 304 us where 16 took 132 and 245); 8 threads
+// along time backwards hold 32 elements in up to 256 registers, two workgroups
+// to a unit, which beats more threads of fewer registers (512 threads of 16
+// elements: 304 us).  Wider tiles (128 channels) and workgroups that stay and
+// fetch their next unit early were slower (267 and 293 us backwards).  Channels
+// past a multiple of 64 cost a whole tile: 8x65536 positions of 64, 65 and 128
+// channels take 323, 501 and 490 us fwd + bwd.
 #include <hip/hip_runtime.h>
 
 #include "gscan_math.h"
@@ -481,8 +483,9 @@ __global__ __launch_bounds__(kCloseChan* kCloseRows) void k_close_dlam(Args g, l
 }
 
 // One position: a thread takes two channels of R sequences, whose loads are
-// under way together and which share the channels' rates.  512 x 4096 bf16: 7.2
-// us, 4.6 TB/s; a single sequence of 384 channels 2.0 us, a launch's latency.
+// under way together and which share the channels' rates.  512 x 4096 bf16: 9
+// us, 3.7 TB/s, as long as the call's host side; a single sequence of 384
+// channels 2.2 us, a launch's latency.
 template <class D, int R>
 __global__ __launch_bounds__(256) void k_step(int B, int C, int S, const typename D::S* x,
                                               long long xs, const typename D::S* r, long long rs,
@@ -624,8 +627,9 @@ hipError_t close_dlam(const Args& a, long long parts, hipStream_t st) {
 }
 
 // Sequences of a thread: one while the threads are too few to fill the device
-// (latency), else four (one and four: 256 x 2048 bf16 3.4 and 4.2 us, 512 x 4096
-// 7.3 and 7.2, 2048 x 4096 23.5 and 21.9).
+// (latency), else four (one and four, on inputs that change from call to call:
+// 256 x 2048 bf16 4.3 and 5.0 us, 512 x 4096 9.4 and 8.9, 2048 x 4096 28.0 and
+// 26.8).
 template <class D>
 static void launch_step(int B, int C, int S, float decay, const gscan_view& x, const gscan_view& r,
                         const gscan_view& i, const float* lam, float* state, const int* slots,
