@@ -198,14 +198,17 @@ class AdamW(torch.optim.Optimizer):
         return dict(super().__getstate__(), **{n: getattr(self, n) for n in self._OPTIONS})
 
     def add_param_group(self, param_group):
-        for n in ("lr", "eps", "weight_decay"):
-            v = param_group.get(n, self.defaults[n])
-            if not isinstance(v, torch.Tensor) and not 0.0 <= v < math.inf:
-                raise ValueError("%s must be finite and not negative, got %r" % (n, v))
         super().add_param_group(param_group)
-        if not all(p.is_contiguous() for p in self.param_groups[-1]["params"]):
+        group, wrong = self.param_groups[-1], None
+        for n in ("lr", "eps", "weight_decay"):
+            v = group[n]
+            if not isinstance(v, torch.Tensor) and not 0.0 <= v < math.inf:
+                wrong = "%s must be finite and not negative, got %r" % (n, v)
+        if not all(p.is_contiguous() for p in group["params"]):
+            wrong = "parameters must be contiguous"
+        if wrong:
             self.param_groups.pop()
-            raise ValueError("parameters must be contiguous")
+            raise ValueError(wrong)
 
     def _new_state(self, p, step):
         if not p.is_contiguous():

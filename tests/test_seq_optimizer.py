@@ -48,3 +48,11 @@ def test_strided_parameters_are_refused_when_they_are_given():
     w = torch.nn.Parameter(torch.zeros(2, 3, 4, 4).to(memory_format=torch.channels_last))
     with pytest.raises(ValueError, match="contiguous"):
         AdamW([w])
+
+
+def test_other_mistakes_are_told_as_by_the_base_class():
+    opt = AdamW([torch.nn.Parameter(torch.zeros(2))])
+    with pytest.raises(TypeError, match="must be a dict"):
+        opt.add_param_group([torch.nn.Parameter(torch.zeros(2))])
+    with pytest.raises(ValueError, match="more than one parameter group"):
+        opt.add_param_group({"params": opt.param_groups[0]["params"]})
