@@ -11,6 +11,12 @@ sequences (``include/gscan.h``, :mod:`aware_conv_amd.gscan`,
 :class:`GatedScan2d`) and the AdamW step over many tensors
 (``include/adamw.h``, :mod:`aware_conv_amd.adamw`, :class:`AdamW`).
 
+For token sequences: a selective state space scan (``include/sscan.h``,
+:func:`selective_scan`), the short causal convolution before it
+(``include/cconv.h``, :func:`causal_conv`) and the root-mean-square norm with the
+residual's addition, also in 8 bits (``include/rmsnorm.h``, :func:`rms_norm`); the
+block of all three is :class:`SelectiveMixer`.
+
 Nothing is imported eagerly, so ``import aware_conv_amd.build`` works before
 the library exists.
 """
@@ -18,14 +24,20 @@ the library exists.
 __all__ = ["WTConv2d", "WTConvFunction", "wtconv_fwd", "wtconv_bwd_input",
            "wtconv_bwd_weight", "wtconv_workspace_size",
            "gscan_fwd", "gscan_bwd", "gscan_step", "gated_scan", "GatedScan2d",
-           "adamw_grad_norm", "adamw_step", "AdamW"]
+           "adamw_grad_norm", "adamw_step", "AdamW",
+           "sscan_fwd", "sscan_bwd", "sscan_step", "selective_scan",
+           "cconv_fwd", "cconv_bwd", "cconv_step", "causal_conv",
+           "rmsnorm_fwd", "rmsnorm_fwd_e4m3", "rmsnorm_bwd", "rms_norm", "SelectiveMixer"]
 
 
 _HOMES = {"_lib": ("wtconv_fwd", "wtconv_bwd_input", "wtconv_bwd_weight",
                    "wtconv_workspace_size", "wtconv_strerror", "make_shape"),
-          "module": ("WTConv2d", "WTConvFunction", "GatedScan2d"),
+          "module": ("WTConv2d", "WTConvFunction", "GatedScan2d", "SelectiveMixer"),
           "gscan": ("gscan_fwd", "gscan_bwd", "gscan_step", "gated_scan", "GatedScanFunction"),
-          "adamw": ("adamw_grad_norm", "adamw_step", "AdamW")}
+          "adamw": ("adamw_grad_norm", "adamw_step", "AdamW"),
+          "sscan": ("sscan_fwd", "sscan_bwd", "sscan_step", "selective_scan", "SelectiveScanFunction"),
+          "cconv": ("cconv_fwd", "cconv_bwd", "cconv_step", "causal_conv", "CausalConvFunction"),
+          "rmsnorm": ("rmsnorm_fwd", "rmsnorm_fwd_e4m3", "rmsnorm_bwd", "rms_norm", "RmsNormFunction")}
 
 
 def __getattr__(name):

@@ -80,6 +80,20 @@ class AdamwConfig(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("lr_dev", "grad_scale_dev", "norm")])
 
 
+# sscan.h, cconv.h and rmsnorm.h: bound in sscan.py, cconv.py and rmsnorm.py
+class SscanShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "D", "N", "G", "dtype")]
+
+
+class CconvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "C", "K", "dtype", "silu")]
+
+
+class RmsnormShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "T", "C", "dtype", "rdtype")] +
+                [("eps", ctypes.c_float)])
+
+
 _gp, _gv = ctypes.POINTER(GscanShape), _vp  # views: addresses of GscanView
 _szp = ctypes.POINTER(ctypes.c_size_t)
 lib.gscan_states_size.argtypes = [_gp, _szp]
@@ -95,15 +109,33 @@ lib.adamw_grad_norm.argtypes = ([ctypes.c_int, _vp, ctypes.c_int, ctypes.c_doubl
                                 [ctypes.c_size_t, _vp])
 lib.adamw_step.argtypes = ([ctypes.POINTER(AdamwConfig), _vp, ctypes.c_int] + [_vp] * 2 +
                            [ctypes.c_size_t, _vp])
+_ssp, _ccp, _rnp = (ctypes.POINTER(t) for t in (SscanShape, CconvShape, RmsnormShape))
+_int, _size = ctypes.c_int, ctypes.c_size_t
+lib.sscan_states_size.argtypes = [_ssp, _szp]
+lib.sscan_workspace_size.argtypes = [_ssp, _int, _szp]
+lib.sscan_fwd.argtypes = [_ssp] + [_vp] * 14 + [_size, _vp]
+lib.sscan_bwd.argtypes = [_ssp] + [_vp] * 22 + [_size, _vp]
+lib.sscan_step.argtypes = [_ssp, _int] + [_vp] * 12
+lib.cconv_workspace_size.argtypes = [_ccp, _szp]
+lib.cconv_fwd.argtypes = [_ccp] + [_vp] * 8
+lib.cconv_bwd.argtypes = [_ccp] + [_vp] * 12 + [_size, _vp]
+lib.cconv_step.argtypes = [_ccp, _int] + [_vp] * 7
+lib.rmsnorm_workspace_size.argtypes = [_rnp, _szp]
+lib.rmsnorm_fwd.argtypes = [_rnp] + [_vp] * 7
+lib.rmsnorm_fwd_e4m3.argtypes = [_rnp] + [_vp] * 8
+lib.rmsnorm_bwd.argtypes = [_rnp] + [_vp] * 9 + [_size, _vp]
+_TOKEN_CALLS = ("sscan_states_size", "sscan_workspace_size", "sscan_fwd", "sscan_bwd", "sscan_step",
+                "cconv_workspace_size", "cconv_fwd", "cconv_bwd", "cconv_step",
+                "rmsnorm_workspace_size", "rmsnorm_fwd", "rmsnorm_fwd_e4m3", "rmsnorm_bwd")
 for _n in ("gscan_states_size", "gscan_workspace_size", "gscan_fwd", "gscan_bwd", "gscan_step",
-           "adamw_workspace_size", "adamw_grad_norm", "adamw_step"):
+           "adamw_workspace_size", "adamw_grad_norm", "adamw_step") + _TOKEN_CALLS:
     getattr(lib, _n).restype = ctypes.c_int
 
 EXPORTED = ("wtconv_workspace_size", "wtconv_fwd", "wtconv_bwd_input",
             "wtconv_bwd_weight", "wtconv_bwd", "wtconv_bwd_noalloc", "wtconv_strerror",
             "dwconv_workspace_size", "dwconv_fwd", "dwconv_bwd",
             "gscan_states_size", "gscan_workspace_size", "gscan_fwd", "gscan_bwd", "gscan_step",
-            "adamw_workspace_size", "adamw_grad_norm", "adamw_step")
+            "adamw_workspace_size", "adamw_grad_norm", "adamw_step") + _TOKEN_CALLS
 
 
 class WTConvError(RuntimeError):

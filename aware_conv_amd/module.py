@@ -1,9 +1,10 @@
 """torch.autograd and nn.Module wrappers over the C ABI."""
 import math
+import operator
 
 import torch
 
-from . import _lib, gscan
+from . import _lib, cconv, gscan, rmsnorm, sscan
 
 
 class WTConvFunction(torch.autograd.Function):
@@ -95,3 +96,103 @@ class GatedScan2d(torch.nn.Module):
         if len(self.lam) == 2:
             h = h + gscan.gated_scan(x, r, i, self.lam[1], reverse=True, decay=self.DECAY)[0]
         return h * self.scale
+
+
+class SelectiveMixer(torch.nn.Module):
+    """Block over token sequences [B, T, C]: the root-mean-square norm of the residual stream, a
+    projection to twice ``expand * channels``, a short causal convolution and a selective state
+    space scan of one half, gated by the other, and a projection back.
+
+    ``forward`` takes the stream as the output x of the block before and what was added up before
+    that (``residual``; None: x starts the stream), and returns its own output and the sum, to be
+    handed on alike.  ``prompt`` also fills rows of a cache, from which ``step`` goes on one
+    position at a time.
+
+    Norm weight, convolution and the scan's parameters are fp32 whatever the layer's dtype; the
+    steps start spread over ``step_range``, the decay rates at 1..states."""
+
+    _FP32 = ("norm", "conv_w", "conv_b", "dt_bias", "a_log", "d")
+
+    def __init__(self, channels, states=16, expand=2, taps=4, rank=None, groups=1, eps=1e-5,
+                 step_range=(1e-3, 1e-1), residual_fp32=False, device=None, dtype=None):
+        super().__init__()
+        f = {"device": device, "dtype": dtype}
+        p = {"device": device, "dtype": torch.float32}
+        inner = expand * channels
+        rank = rank or max(1, channels // 16)
+        self.split = (rank, groups * states, groups * states)
+        self.eps, self.residual_fp32 = eps, residual_fp32
+        self.inner = torch.nn.Linear(channels, 2 * inner, bias=False, **f)
+        self.low = torch.nn.Linear(inner, sum(self.split), bias=False, **f)
+        self.dt = torch.nn.Linear(rank, inner, bias=False, **f)
+        self.outer = torch.nn.Linear(inner, channels, bias=False, **f)
+        self.norm = torch.nn.Parameter(torch.ones(channels, **p))
+        self.conv_w = torch.nn.Parameter(torch.empty(inner, taps, **p).uniform_(-1, 1) / math.sqrt(taps))
+        self.conv_b = torch.nn.Parameter(torch.zeros(inner, **p))
+        lo, hi = (math.log(s) for s in step_range)
+        step = torch.exp(torch.linspace(lo, hi, inner, dtype=torch.float64))
+        self.dt_bias = torch.nn.Parameter(torch.log(torch.expm1(step)).float().to(device))
+        rate = torch.arange(1, states + 1, dtype=torch.float32).log()
+        self.a_log = torch.nn.Parameter(rate.repeat(inner, 1).to(device))
+        self.d = torch.nn.Parameter(torch.ones(inner, **p))
+
+    def _apply(self, fn, recurse=True):
+        """Conversions of the layer (half(), to(dtype), ...) move the parameters that stay in fp32
+        and leave their dtype."""
+        own = [t for n in self._FP32 for t in (getattr(self, n), getattr(self, n).grad) if t is not None]
+
+        def converted(t):
+            new = fn(t)
+            return t.to(new.device) if any(t is k for k in own) and new.dtype != t.dtype else new
+
+        return super()._apply(converted, recurse)
+
+    def _stream(self, x, residual):
+        """The residual that the norm adds x to: in fp32 from the block that starts the stream on."""
+        if residual is None and self.residual_fp32:
+            return torch.zeros_like(x, dtype=torch.float32)
+        return residual
+
+    def _mix(self, x, residual, lengths, conv0=None, h0=None):
+        """(output, stream, the convolution's last inputs, the scan's last state)"""
+        y, total = rmsnorm.rms_norm(x, self.norm, self._stream(x, residual), self.eps)
+        u, z = self.inner(y).chunk(2, dim=-1)
+        u, last = cconv.causal_conv(u, self.conv_w, self.conv_b, h0=conv0, lengths=lengths)
+        dt, b, c = self.low(u).split(self.split, dim=-1)
+        v, h = sscan.selective_scan(u, self.dt(dt), self.a_log, b, c, self.d, z, self.dt_bias, h0, lengths)
+        return self.outer(v), x if total is None else total, last, h
+
+    def forward(self, x, residual=None, lengths=None):
+        """(output, residual stream) of x [B, T, C]; lengths [B] int32 where sequences are padded."""
+        return self._mix(x, residual, lengths)[:2]
+
+    def new_cache(self, rows):
+        """Zeroed rows for ``prompt`` and ``step``: the convolution's inputs and the scan's states."""
+        inner, taps = self.conv_w.shape
+        f = {"device": self.a_log.device}
+        return (torch.zeros(rows, taps - 1, inner, dtype=self.inner.weight.dtype, **f),
+                torch.zeros(rows, inner, self.a_log.shape[1], **f))
+
+    @torch.no_grad()
+    def prompt(self, x, cache, residual=None, lengths=None, rows=None):
+        """``forward`` from what rows of the cache hold (``rows``: their numbers, a list of integers;
+        the first B if None), which then hold what ``step`` goes on from."""
+        conv, state = cache
+        rows = list(range(x.shape[0])) if rows is None else [operator.index(k) for k in rows]
+        if len(rows) != x.shape[0] or len(set(rows)) != len(rows) or not all(0 <= k < len(state) for k in rows):
+            raise ValueError("rows must be %d different rows of the cache's %d, got %s"
+                             % (x.shape[0], len(state), rows))
+        at = torch.tensor(rows, dtype=torch.long, device=state.device)
+        out, total, conv[at], state[at] = self._mix(x, residual, lengths, conv[at], state[at])
+        return out, total
+
+    @torch.no_grad()
+    def step(self, x, cache, residual=None, slots=None):
+        """(output, residual stream) of one position x [B, C], which moves the cache's rows on."""
+        y, total, _ = rmsnorm.rmsnorm_fwd(x, self.norm, residual=self._stream(x, residual), eps=self.eps)
+        u, z = self.inner(y).chunk(2, dim=-1)
+        u = cconv.cconv_step(u, self.conv_w, cache[0], bias=self.conv_b, slots=slots)
+        dt, b, c = self.low(u).split(self.split, dim=-1)
+        v = sscan.sscan_step(u, self.dt(dt), self.a_log, b, c, cache[1], d=self.d, z=z, dt_bias=self.dt_bias,
+                             slots=slots)
+        return self.outer(v), x if total is None else total

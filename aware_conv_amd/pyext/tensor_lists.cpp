@@ -130,21 +130,22 @@ PyObject* views(PyObject* args) {
     return PyLong_FromLong(-1);
 }
 
-// flat(tensor, dtype, device, n0, n1) -> address, None for None, False if it
-// does not fit: contiguous, of that dtype on that CUDA device, of the shape
-// (n0, n1), or (n0,) for a negative n1.
+// flat(tensor, dtype, device, n0, n1[, n2]) -> address, None for None, False if
+// it does not fit: contiguous, of that dtype on that CUDA device, of the shape
+// (n0, n1, n2), (n0, n1) without n2, or (n0,) for a negative n1.
 PyObject* flat(PyObject* args) {
     PyObject *o, *dtype;
     int device;
-    long long n0, n1;
-    if (!PyArg_ParseTuple(args, "OOiLL", &o, &dtype, &device, &n0, &n1)) return nullptr;
+    long long n0, n1, n2 = -1;
+    if (!PyArg_ParseTuple(args, "OOiLL|L", &o, &dtype, &device, &n0, &n1, &n2)) return nullptr;
     if (o == Py_None) Py_RETURN_NONE;
     if (!THPVariable_Check(o) || !THPDtype_Check(dtype)) Py_RETURN_FALSE;
     const at::Tensor& t = THPVariable_Unpack(o);
-    const int dims = n1 < 0 ? 1 : 2;
+    const int dims = n1 < 0 ? 1 : n2 < 0 ? 2 : 3;
     if (t.scalar_type() != reinterpret_cast<THPDtype*>(dtype)->scalar_type || !t.is_cuda() ||
         t.device().index() != device || t.layout() != at::kStrided || t.dim() != dims ||
-        t.size(0) != n0 || (dims == 2 && t.size(1) != n1) || !t.is_contiguous())
+        t.size(0) != n0 || (dims > 1 && t.size(1) != n1) || (dims > 2 && t.size(2) != n2) ||
+        !t.is_contiguous())
         Py_RETURN_FALSE;
     return PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.data_ptr()));
 }
