@@ -34,10 +34,22 @@ int check_shape(const sscan_shape* s) {
 class Bufs : public calls::Bufs {
   public:
     Bufs(const sscan_shape& s, long long T) : s_(s), T_(T), e_(elem_size(s.dtype)) {}
-    void wide(const gscan_view* v, bool out) { view(v, s_.B, T_, s_.D, e_, out); }
-    void low(const gscan_view* v, bool out) { view(v, s_.B, T_, (long long)s_.G * s_.N, e_, out); }
+    void wide(const gscan_view* v, bool out) { act(v, s_.D, out); }
+    void low(const gscan_view* v, bool out) { act(v, (long long)s_.G * s_.N, out); }
+    // what is wrong, stride too far last
+    int done() const {
+        const int rc = calls::Bufs::done();
+        return rc ? rc : far_ ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
+    }
 
   private:
+    void act(const gscan_view* v, long long run, bool out) {
+        view(v, s_.B, T_, run, e_, out);
+        if (v && T_ > 1 && v->sr > kMaxStride) far_ = true;
+    }
+    // 15 rows are within 32 bits of bytes
+    static constexpr long long kMaxStride = 1LL << 26;
+    bool far_ = false;
     const sscan_shape& s_;
     long long T_;
     size_t e_;
@@ -51,7 +63,6 @@ ssc::Args args_of(const sscan_shape& s) {
     a.N = s.N;
     a.G = s.G;
     a.Dg = s.D / s.G;
-    a.tiles = (a.Dg + 63) / 64;
     return a;
 }
 

@@ -1,9 +1,9 @@
 // Backward pass of the selective scan (include/sscan.h).
 //
-// A workgroup takes 64 channels of a sequence (or of a segment of it), a
-// wavefront 16 of them, from the last chunk of positions to the first.  In a
-// chunk it forms the states again from the saved one, keeps those of up to 64 / NP
-// positions in registers, and runs the gradient back over them.
+// A workgroup takes its channels of a sequence (or of a segment of it) from the last
+// chunk of positions to the first.  In a chunk it forms the states again from the
+// saved one, keeps those of 16 positions (8 where a lane has 4 states) in
+// registers, and runs the gradient back over them.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -13,280 +13,313 @@
 namespace ssc {
 namespace {
 
-constexpr int kWaves = 4;
-
-template <int NP>
-struct Form {
-    static constexpr int kChunk = NP == 16 ? 16 : 32;         // positions between saved states
-    static constexpr int kTiles = kChunk / 16;
-    static constexpr int kSub = NP <= 4 ? 16 : 64 / NP;       // positions whose states are in registers
-    static constexpr int kSubs = kChunk / kSub;
-    static constexpr int kOwn = kChunk / 4;                   // positions that a lane reads and writes
-    static constexpr int kRow = kChunk + 1;                   // float4s between two channels in LDS
-    static constexpr int kStates = 4 * NP;
-};
-
-// The sum of v over the 16 lanes of a row, in every lane.
-__device__ __forceinline__ float row_sum(float v) {
-    auto dpp = [](float x, auto ctrl) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value,
-                                                                  0xf, 0xf, true));
-    };
-    v += dpp(v, std::integral_constant<int, 0x128>{});  // row_ror:8
-    v += dpp(v, std::integral_constant<int, 0x124>{});  // row_ror:4
-    v += dpp(v, std::integral_constant<int, 0x122>{});
-    v += dpp(v, std::integral_constant<int, 0x121>{});
-    return v;
-}
-
-// Addresses of one lane's channel, and the parameters of its states.
-template <class D, int NP>
-struct Lane {
-    using S = typename D::S;
-    int row, i, seq, s, group, d, n, t_lo, t_end, t_hi;
-    bool live, whole;
-    long long states_at, all;
-    const S *x, *dt, *z, *dy, *b, *c;
-    float a2[NP], bias;
-    bool there[NP];
-    __device__ __forceinline__ Lane(const Args& a, int lane, int wave, int unit) {
-        row = lane >> 4;
-        i = lane & 15;
-        const int tiles = a.G * a.tiles, tile = unit % tiles, rest = unit / tiles;
-        seq = rest / a.S;
-        s = rest % a.S;
-        group = tile / a.tiles;
-        const int c0 = (tile % a.tiles) * 64 + wave * 16;
-        live = c0 + i < a.Dg;
-        d = group * a.Dg + min(c0 + i, a.Dg - 1);
-        n = a.lengths ? min(max(a.lengths[seq], 0), a.T) : a.T;
-        t_lo = s * a.seg;
-        t_end = min(a.T - t_lo, a.seg) + t_lo;
-        t_hi = min(t_end, n);
-        whole = a.N == 4 * NP;
-        states_at = ((long long)seq * a.D + d) * a.N;
-        all = (long long)a.B * a.D * a.N;
-        x = (const S*)a.x + seq * a.x_sb + d;
-        dt = (const S*)a.dt + seq * a.dt_sb + d;
-        z = (const S*)a.z + seq * a.z_sb + d;
-        dy = (const S*)a.dy + seq * a.dy_sb + d;
-        b = (const S*)a.b + seq * a.b_sb + group * a.N;
-        c = (const S*)a.c + seq * a.c_sb + group * a.N;
-        bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-            const int m = row * NP + j;
-            there[j] = m < a.N;
-            a2[j] = there[j] ? -kLog2e * expf(a.a_log[(long long)d * a.N + min(m, a.N - 1)]) : 0.f;
-        }
-    }
-};
+constexpr std::true_type whole{};   // of tiles that have all their positions
+constexpr std::false_type some{};
+constexpr int kPad2 = 18;          // float2s between two channels in LDS: no bank conflicts
+constexpr int kPad4 = kChunk + 1;  // and float4s
 
 __device__ __forceinline__ float dsilu(float z, float k) { return k * fmaf(z, 1.f - k, 1.f); }
 
 // What a segment makes of a gradient that comes from behind it, r = exp(delta A) g
 // of its first position, from zero; and its sum of delta.
-template <class D, int NP, bool GATE>
-__global__ __launch_bounds__(64 * kWaves) void k_back(Args a) {
-    __shared__ float2 lds[kWaves][16 * 18];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Lane<D, NP> l(a, lane, wave, blockIdx.x);
+template <class D, class F, bool GATE>
+__global__ __launch_bounds__(F::kThreads) void k_back(Args a) {
+    using S = typename D::S;
+    constexpr int NP = F::NP, NB = F::NB, kSlots = F::kSlots;
+    __shared__ float2 staged[2][F::kChannels * kPad2];
+    const Lane<F> l(a);
     if (l.t_lo >= l.t_hi || l.s == 0) return;  // nothing comes before the first segment
-    float2* const mine = lds[wave] + l.i * 18;
-    float r[NP] = {}, sum = 0.f;
-    for (int t0 = l.t_lo + (l.t_hi - 1 - l.t_lo) / 16 * 16; t0 >= l.t_lo; t0 -= 16) {
-        float c[NP];
-        const long long tc = min(t0 + l.i, l.n - 1);
-        load_states<D, NP>(c, l.c + tc * a.c_sr, l.row * NP, a.N, l.whole, t0 + l.i < l.t_hi);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const bool valid = t0 + 4 * k + l.row < l.t_hi && l.live;
-            const long long t = min(t0 + 4 * k + l.row, l.n - 1);
-            const float delta = valid ? softplus(gsc::load_one<D>(l.dt + t * a.dt_sr) + l.bias).delta : 0.f;
-            float ds = valid ? gsc::load_one<D>(l.dy + t * a.dy_sr) : 0.f;
-            if constexpr (GATE) {
-                const float z = gsc::load_one<D>(l.z + t * a.z_sr);
-                ds = valid ? ds * (z * sig(z)) : 0.f;
-            }
-            sum += delta;
-            mine[4 * k + l.row] = make_float2(delta, ds);
+    const int first_t = l.io_base + l.io_row;
+    const bool last_slot = l.last_slot;
+    const int t_last = l.t_lo + (l.t_hi - 1 - l.t_lo) / kChunk * kChunk;
+    auto wide = [&](const void* p, long long sb, long long sr) {
+        return Rows<S>(p, sb, sr, l.seq, t_last + l.io_base, l.d0, l.io_row, l.io_ch);
+    };
+    Rows<S> dt_ = wide(a.dt, a.dt_sb, a.dt_sr), z_ = wide(a.z, a.z_sb, a.z_sr), dy_ = wide(a.dy, a.dy_sb, a.dy_sr);
+    Rows<S> c_(a.c, a.c_sb, a.c_sr, l.seq, t_last, l.group * a.N, l.i, 0);
+    float r[NP] = {}, sum = 0.f, cs[NP];
+    Column<D, F> dt, dy, z;
+    States<D, NP> c;
+    auto load = [&](auto full, int n) {
+        if constexpr (full) {
+            dt.load(dt_, last_slot);
+            dy.load(dy_, last_slot);
+            if constexpr (GATE) z.load(z_, last_slot);
+            c.load(c_.at(0), l);
+        } else {
+            dt.load_some(dt_, last_slot, n - first_t);
+            dy.load_some(dy_, last_slot, n - first_t);
+            if constexpr (GATE) z.load_some(z_, last_slot, n - first_t);
+            c.clear();
+            if (l.i < n) c.load(c_.at(0), l);
         }
-        wave_sync();
-        unroll<16>([&](auto K) {
-            constexpr int k = 15 - K;
-            const float2 q = mine[k];
+        dt_.move(-kChunk);
+        dy_.move(-kChunk);
+        if constexpr (GATE) z_.move(-kChunk);
+        c_.move(-kChunk);
+    };
+    auto stage = [&](auto full, float2* to, int n) {
 #pragma unroll
-            for (int j = 0; j < NP; ++j)
-                r[j] = decay(q.x, l.a2[j]) * fmaf(bcast<k>(c[j]), q.y, r[j]);
+        for (int j = 0; j < NP; ++j) {
+            cs[j] = c[j];
+            now(cs[j]);
+        }
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            if ((q + 1) * F::kStep > 16 && !last_slot) continue;
+            const int t = first_t + F::kStep * q;
+            const bool valid = full || t < n;
+            const float delta = valid ? softplus(dt[q] + l.bias).delta : 0.f;
+            float ds = dy[q];
+            if constexpr (GATE) ds *= z[q] * sig(z[q]);
+            sum += delta;
+            to[l.io_at * kPad2 + t] = make_float2(delta, valid ? ds : 0.f);
+        }
+    };
+    int half = 0;
+    // full: two more chunks come before this one
+    auto turn = [&](auto full, int t0) {
+        const float2* const mine = staged[half] + (l.ct * 16 + l.i) * kPad2;
+        float2 m[16];
+        unroll<4>([&](auto K) {
+            constexpr int k = 3 - K;
+            float e[4][NP];
+            unroll<4>([&](auto L) {
+                constexpr int q = 4 * k + L;
+                m[q] = mine[q];
+#pragma unroll
+                for (int j = 0; j < NP; ++j) e[L][j] = decay(m[q].x, l.a2[j]);
+            });
+            unroll<4>([&](auto L) {
+                constexpr int q = 3 - L;
+                add_bcast<4 * k + q>(r, cs, m[4 * k + q].y);
+#pragma unroll
+                for (int j = 0; j < NP; ++j) r[j] *= e[q][j];
+            });
         });
-        wave_sync();
-    }
-    if (!l.live) return;
+        if (full || t0 > l.t_lo) stage(whole, staged[half ^ 1], kChunk);
+        if (full || t0 > l.t_lo + kChunk) load(whole, kChunk);
+        lds_barrier();
+        half ^= 1;
+    };
+    load(some, l.t_hi - t_last);
+    stage(some, staged[0], l.t_hi - t_last);
+    if (t_last > l.t_lo) load(whole, kChunk);
+    lds_barrier();
+    loads_done();
+    int t0 = t_last;
+    for (; t0 > l.t_lo + kChunk; t0 -= kChunk) turn(whole, t0);
+    for (; t0 >= l.t_lo; t0 -= kChunk) turn(some, t0);
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
-        if (l.there[j]) a.seg_state[l.s * l.all + l.states_at + l.row * NP + j] = r[j];
-    const float total = sum_rows(sum, sum, sum, sum);
-    if (l.row == 0) a.seg_sum[((long long)l.s * a.B + l.seq) * a.D + l.d] = total;
+    for (int j = 0; j < NP; ++j) a.seg_state[l.s * l.all + l.states_at + l.at[j]] = r[j];
+    const float total = over_channel<F>(sum, reinterpret_cast<float*>(staged));
+    if (threadIdx.x < F::kChannels) a.seg_sum[((long long)l.s * a.B + l.seq) * a.D + l.io_d] = total;
 }
 
-template <class D, int NP, bool GATE>
-__global__ __launch_bounds__(64 * kWaves) void k_bwd(Args a) {
+template <class D, class F, bool GATE>
+__global__ __launch_bounds__(F::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_bwd(Args a) {
     using S = typename D::S;
-    using F = Form<NP>;
-    __shared__ float4 lds[kWaves][16 * F::kRow];                // delta, u, ds, dy silu'(z)
-    __shared__ float bc[kWaves][F::kChunk][2][F::kStates];       // sums of db and dc over 16 channels
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Lane<D, NP> l(a, lane, wave, blockIdx.x);
-    const int tile = (blockIdx.x % (a.G * a.tiles)) % a.tiles;
-    S* const dx_ = (S*)a.dx + l.seq * a.dx_sb + l.d;
-    S* const ddt_ = (S*)a.ddt + l.seq * a.ddt_sb + l.d;
-    S* const dz_ = (S*)a.dz + l.seq * a.dz_sb + l.d;
-    if (l.live)
-        for (int t = max(l.n, l.t_lo) + l.row; t < l.t_end; t += 4) {
-            gsc::store_one<D>(dx_ + t * a.dx_sr, 0.f);
-            gsc::store_one<D>(ddt_ + t * a.ddt_sr, 0.f);
-            if constexpr (GATE) gsc::store_one<D>(dz_ + t * a.dz_sr, 0.f);
+    constexpr int NP = F::NP, NB = F::NB, kSlots = F::kSlots;
+    // positions whose states are in registers
+    constexpr int kSub = NP <= 2 ? 16 : 8, kSubs = 16 / kSub;
+    constexpr int kWidth = F::kStates + 1;
+    __shared__ float4 staged[F::kChannels * kPad4];         // delta, u, ds
+    __shared__ float parts[3][NB][16 * F::kChannels];       // sums over states: of g b, A q and c h
+    __shared__ float2 bc[F::CT][kChunk * kWidth];           // sums over 16 channels: of db and dc
+    const Lane<F> l(a);
+    const int first_t = l.io_base + l.io_row;  // the thread's first position of a chunk
+    const bool last_slot = l.last_slot;
+    if (max(l.n, l.t_lo) < l.t_end) {  // zeros behind the sequence
+        S* const x0 = (S*)a.dx + l.seq * a.dx_sb + l.io_d;
+        S* const t0 = (S*)a.ddt + l.seq * a.ddt_sb + l.io_d;
+        S* const z0 = (S*)a.dz + l.seq * a.dz_sb + l.io_d;
+        for (int t = max(l.n, l.t_lo) + first_t; t < l.t_end; t += F::kStep) {
+            gsc::store_one<D>(x0 + t * a.dx_sr, 0.f);
+            gsc::store_one<D>(t0 + t * a.ddt_sr, 0.f);
+            if constexpr (GATE) gsc::store_one<D>(z0 + t * a.dz_sr, 0.f);
         }
+    }
 
+    const bool io_there = l.io_ch == l.io_at;
     float r[NP];  // exp(delta A) g of the position behind
     // the sum over positions of delta q, of a chunk and, with what its additions lost, of all
     float da[NP], da_all[NP] = {}, da_lost[NP] = {};
-    const bool some = l.t_lo < l.t_hi;
+    const bool any = l.t_lo < l.t_hi;
 #pragma unroll
     for (int j = 0; j < NP; ++j)
-        r[j] = a.dh_last && l.there[j] && l.live && (some || l.s == 0)
-                   ? a.dh_last[l.states_at + l.row * NP + j] : 0.f;
-    if (some && l.live) {
+        r[j] = a.dh_last && l.there[j] && l.live && (any || l.s == 0) ? a.dh_last[l.states_at + l.at[j]] : 0.f;
+    if (any) {
         // the segments behind, from the last one that has positions
         for (int k = (l.n - 1) / a.seg; k > l.s; --k) {
             const float sum = a.seg_sum[((long long)k * a.B + l.seq) * a.D + l.d];
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
-                const float own = a.seg_state[k * l.all + l.states_at + min(l.row * NP + j, a.N - 1)];
-                r[j] = l.there[j] ? fmaf(exp2_hw(sum * l.a2[j]), r[j], own) : 0.f;
+                const float own = a.seg_state[k * l.all + l.states_at + l.at[j]];
+                r[j] = l.there[j] && l.live ? fmaf(exp2_hw(sum * l.a2[j]), r[j], own) : 0.f;
             }
         }
     }
-    const float skip = a.d ? a.d[l.d] : 0.f;
+    const float skip = a.d ? a.d[l.io_d] : 0.f;
     float dd = 0.f, dbias = 0.f;
-    float4* const mine = lds[wave] + l.i * F::kRow;
+    const float4* const mine = staged + (l.ct * 16 + l.i) * kPad4;
+    const int quad = l.i & 3;
+    const int last = any ? (l.t_hi - 1) / kChunk : -1, first = l.t_lo / kChunk, t_last = max(last, 0) * kChunk;
+    auto wide = [&](const void* p, long long sb, long long sr) {
+        return Rows<S>(p, sb, sr, l.seq, t_last + l.io_base, l.d0, l.io_row, l.io_ch);
+    };
+    Rows<S> x_ = wide(a.x, a.x_sb, a.x_sr), dt_ = wide(a.dt, a.dt_sb, a.dt_sr), dy_ = wide(a.dy, a.dy_sb, a.dy_sr);
+    Rows<S> z_ = wide(a.z, a.z_sb, a.z_sr), dx_ = wide(a.dx, a.dx_sb, a.dx_sr), ddt_ = wide(a.ddt, a.ddt_sb, a.ddt_sr);
+    Rows<S> dz_ = wide(a.dz, a.dz_sb, a.dz_sr);
+    Rows<S> b_(a.b, a.b_sb, a.b_sr, l.seq, t_last, l.group * a.N, l.i, 0), c_(a.c, a.c_sb, a.c_sr, l.seq, t_last, l.group * a.N, l.i, 0);
+    const float* states_ = a.states + saved_at(a, l, max(last, 0));
+    const long long states_step = saved_at(a, l, 1) - saved_at(a, l, 0);
+    const long long width = 2LL * a.G * F::kStates;
+    float* part_ = a.part_bc + (((long long)l.tile * a.B + l.seq) * a.T + t_last) * width + 2LL * l.group * F::kStates;
 
-    const int last = some ? (l.t_hi - 1) / F::kChunk : -1, first = l.t_lo / F::kChunk;
-    for (int chunk = last; chunk >= first; --chunk) {
-        const int t0 = chunk * F::kChunk;
-        float h[NP];
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-            da[j] = 0.f;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-            h[j] = l.there[j] ? a.states[chunk * l.all + l.states_at + min(l.row * NP + j, a.N - 1)] : 0.f;
-        float b[F::kTiles][NP], c[F::kTiles][NP];
-#pragma unroll
-        for (int k = 0; k < F::kTiles; ++k) {
-            const bool valid = t0 + 16 * k + l.i < l.t_hi;
-            const long long t = min(t0 + 16 * k + l.i, l.n - 1);
-            load_states<D, NP>(b[k], l.b + t * a.b_sr, l.row * NP, a.N, l.whole, valid);
-            load_states<D, NP>(c[k], l.c + t * a.c_sr, l.row * NP, a.N, l.whole, valid);
-        }
-        float xs[F::kOwn], slope[F::kOwn];
-#pragma unroll
-        for (int k = 0; k < F::kOwn; ++k) {
-            const bool valid = t0 + 4 * k + l.row < l.t_hi && l.live;
-            const long long t = min(t0 + 4 * k + l.row, l.n - 1);
-            xs[k] = gsc::load_one<D>(l.x + t * a.x_sr);
-            const Step q = softplus(gsc::load_one<D>(l.dt + t * a.dt_sr) + l.bias);
-            const float dy = gsc::load_one<D>(l.dy + t * a.dy_sr);
-            float ds = dy, dzf = 0.f;
-            if constexpr (GATE) {
-                const float z = gsc::load_one<D>(l.z + t * a.z_sr), way = sig(z);
-                ds = dy * (z * way);
-                dzf = dy * dsilu(z, way);
+    // What is read of a chunk, of n positions (`full`: all 16).
+    Column<D, F> x, dt, dy, z;
+    float saved[NP];
+    States<D, NP> raw_b, raw_c;
+    auto load = [&](auto full, int n) {
+        if constexpr (full) {
+            x.load(x_, last_slot);
+            dt.load(dt_, last_slot);
+            dy.load(dy_, last_slot);
+            if constexpr (GATE) z.load(z_, last_slot);
+            raw_b.load(b_.at(0), l);
+            raw_c.load(c_.at(0), l);
+        } else {
+            x.load_some(x_, last_slot, n - first_t);
+            dt.load_some(dt_, last_slot, n - first_t);
+            dy.load_some(dy_, last_slot, n - first_t);
+            if constexpr (GATE) z.load_some(z_, last_slot, n - first_t);
+            raw_b.clear();
+            raw_c.clear();
+            if (l.i < n) {
+                raw_b.load(b_.at(0), l);
+                raw_c.load(c_.at(0), l);
             }
-            slope[k] = q.slope;
-            mine[4 * k + l.row] = valid ? make_float4(q.delta, q.delta * xs[k], ds, dzf)
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        wave_sync();
+#pragma unroll
+        for (int j = 0; j < NP; ++j) saved[j] = states_[64 * j];
+        x_.move(-kChunk);
+        dt_.move(-kChunk);
+        dy_.move(-kChunk);
+        if constexpr (GATE) z_.move(-kChunk);
+        b_.move(-kChunk);
+        c_.move(-kChunk);
+        states_ -= states_step;
+    };
+    // One chunk's turn.  full: it is whole and another comes before it, so that what is in flight
+    // at each point is known, and nothing is waited for before it is used.
+    auto turn = [&](auto full, int n, bool more) {
+        float start[kSubs][NP], b[NP], c[NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            da[j] = 0.f;
+            start[0][j] = saved[j];
+            b[j] = raw_b[j];
+            c[j] = l.there[j] ? raw_c[j] : 0.f;
+            now(start[0][j]);
+            now(b[j]);
+            now(c[j]);
+        }
+        // the lane's own elements; the others' part of them goes to LDS
+        float xs[kSlots], slope[kSlots], delta[kSlots], ds[kSlots], dzf[kSlots];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            if ((q + 1) * F::kStep > 16 && !last_slot) continue;
+            const int t = first_t + F::kStep * q;
+            const bool valid = full || t < n;
+            const Step v = softplus(dt[q] + l.bias);
+            xs[q] = x[q];
+            now(xs[q]);
+            slope[q] = v.slope;
+            delta[q] = valid ? v.delta : 0.f;
+            ds[q] = dy[q];
+            if constexpr (GATE) {
+                const float way = sig(z[q]);
+                ds[q] = dy[q] * (z[q] * way);
+                dzf[q] = dy[q] * dsilu(z[q], way);
+                now(dzf[q]);
+            }
+            ds[q] = valid ? ds[q] : 0.f;
+            now(ds[q]);
+            // a channel that is not there counts for nothing in sums over channels
+            staged[l.io_at * kPad4 + t] = make_float4(delta[q], valid && io_there ? delta[q] * xs[q] : 0.f, io_there ? ds[q] : 0.f, 0.f);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (full || more) load(whole, kChunk);
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
         // the states that the pieces start from
-        float start[F::kSubs][NP];
-        unroll<F::kSubs>([&](auto Q) {
+        unroll<kSubs - 1>([&](auto Q) {
             constexpr int q = Q;
 #pragma unroll
-            for (int j = 0; j < NP; ++j) start[q][j] = h[j];
-            if constexpr (q + 1 < F::kSubs)
-                unroll<F::kSub>([&](auto K) {
-                    constexpr int t = q * F::kSub + K;
-                    const float4 m = mine[t];
+            for (int j = 0; j < NP; ++j) start[q + 1][j] = start[q][j];
+            unroll<kSub>([&](auto K) {
+                constexpr int t = q * kSub + K;
+                const float4 m = mine[t];
 #pragma unroll
-                    for (int j = 0; j < NP; ++j)
-                        h[j] = fmaf(decay(m.x, l.a2[j]), h[j], bcast<t % 16>(b[t / 16][j]) * m.y);
-                });
+                for (int j = 0; j < NP; ++j)
+                    start[q + 1][j] = fmaf(decay(m.x, l.a2[j]), start[q + 1][j], bcast<t>(b[j]) * m.y);
+            });
         });
-        unroll<F::kSubs>([&](auto Q) {
-            constexpr int q = F::kSubs - 1 - Q;
-            float e[F::kSub][NP], before[F::kSub + 1][NP], part[F::kSub];
+        unroll<kSubs>([&](auto Q) {
+            constexpr int q = kSubs - 1 - Q;
+            float e[kSub][NP], before[kSub + 1][NP];
 #pragma unroll
             for (int j = 0; j < NP; ++j) before[0][j] = start[q][j];
-            unroll<F::kSub>([&](auto K) {
-                constexpr int k = K, t = q * F::kSub + k;
-                const float4 m = mine[t];
-                part[k] = 0.f;
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    e[k][j] = decay(m.x, l.a2[j]);
-                    before[k + 1][j] = fmaf(e[k][j], before[k][j], bcast<t % 16>(b[t / 16][j]) * m.y);
-                    if constexpr (GATE) part[k] = fmaf(bcast<t % 16>(c[t / 16][j]), before[k + 1][j], part[k]);
-                }
-            });
-            unroll<F::kSub / 4>([&](auto V) {
-                constexpr int four = F::kSub / 4 - 1 - V;
-                float gb[4] = {}, qa[4] = {};
-                float pb[4][NP], pc[4][NP];
+            unroll<kSub / 4>([&](auto V) {
+                constexpr int four = V;
+                float part[4];
                 unroll<4>([&](auto L) {
-                    constexpr int w = 3 - L, k = 4 * four + w, t = q * F::kSub + k;
+                    constexpr int k = 4 * four + L, t = q * kSub + k;
                     const float4 m = mine[t];
 #pragma unroll
                     for (int j = 0; j < NP; ++j) {
-                        const float g = fmaf(bcast<t % 16>(c[t / 16][j]), m.z, r[j]);
-                        pb[w][j] = g * m.y;
+                        e[k][j] = decay(m.x, l.a2[j]);
+                        before[k + 1][j] = fmaf(e[k][j], before[k][j], bcast<t>(b[j]) * m.y);
+                    }
+                    if constexpr (GATE) part[L] = sum_bcast<t>(c, before[k + 1]);
+                });
+                if constexpr (GATE)
+                    parts[2][l.nb][(q * kSub + 4 * four + l.row) * F::kChannels + l.ct * 16 + l.i] = sum_rows(part[0], part[1], part[2], part[3]);
+                __builtin_amdgcn_sched_barrier(0);  // keeps registers few
+            });
+            unroll<kSub / 4>([&](auto V) {
+                constexpr int four = kSub / 4 - 1 - V, t4 = q * kSub + 4 * four;
+                asm volatile("" ::: "memory");  // the positions' values are read again, not kept in registers
+                float gb[4], qa[4] = {}, pb[4][NP], pc[4][NP];
+                unroll<4>([&](auto L) {
+                    constexpr int w = 3 - L, k = 4 * four + w, t = q * kSub + k;
+                    const float4 m = mine[t];
+                    add_bcast<t>(r, c, m.z);  // r is g now
+                    gb[w] = sum_bcast<t>(b, r);
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        pb[w][j] = r[j] * m.y;
                         pc[w][j] = before[k + 1][j] * m.z;
-                        gb[w] = fmaf(bcast<t % 16>(b[t / 16][j]), g, gb[w]);
-                        r[j] = g * e[k][j];
+                        r[j] *= e[k][j];
                         const float v = r[j] * before[k][j];
                         da[j] = fmaf(v, m.x, da[j]);
                         qa[w] = fmaf(v, l.a2[j], qa[w]);
                     }
                 });
-                constexpr int t4 = q * F::kSub + 4 * four, own = t4 / 4;
-                unroll<4>([&](auto W) {
+                const int at = (t4 + l.row) * F::kChannels + l.ct * 16 + l.i;
+                parts[0][l.nb][at] = sum_rows(gb[0], gb[1], gb[2], gb[3]);
+                parts[1][l.nb][at] = sum_rows(qa[0], qa[1], qa[2], qa[3]);
+                // lane 4 k + q has position k's sums, the same as its three neighbours, of which
+                // it writes the q-th
 #pragma unroll
-                    for (int j = 0; j < NP; ++j) {
-                        const float sb = row_sum(pb[W][j]), sc = row_sum(pc[W][j]);
-                        if (l.i == 0) {
-                            bc[wave][t4 + W][0][l.row * NP + j] = sb;
-                            bc[wave][t4 + W][1][l.row * NP + j] = sc;
-                        }
-                    }
-                });
-                const float wgb = sum_rows(gb[0], gb[1], gb[2], gb[3]);
-                const float wqa = sum_rows(qa[0], qa[1], qa[2], qa[3]);
-                const float4 m = mine[t4 + l.row];
-                const int t = t0 + t4 + l.row;
-                const float dxv = fmaf(skip, m.z, m.x * wgb);
-                const float ddv = fmaf(xs[own], wgb, kLn2 * wqa) * slope[own];
-                float dzv = 0.f;
-                if constexpr (GATE) {
-                    const float sums = sum_rows(part[4 * four], part[4 * four + 1], part[4 * four + 2], part[4 * four + 3]);
-                    dzv = m.w * fmaf(skip, xs[own], sums);
-                }
-                if (t < l.t_hi && l.live) {
-                    gsc::store_one<D>(dx_ + t * a.dx_sr, dxv);
-                    gsc::store_one<D>(ddt_ + t * a.ddt_sr, ddv);
-                    if constexpr (GATE) gsc::store_one<D>(dz_ + t * a.dz_sr, dzv);
-                    dd = fmaf(m.z, xs[own], dd);
-                    dbias += ddv;
-                }
+                for (int j = 0; j < NP; ++j)
+                    sum_lanes(pb[0][j], pb[1][j], pb[2][j], pb[3][j], pc[0][j], pc[1][j], pc[2][j], pc[3][j]);
+                float2 v = make_float2(pb[0][0], pc[0][0]);
+#pragma unroll
+                for (int k = 1; k < NP; ++k)
+                    if (quad == k) v = make_float2(pb[0][k], pc[0][k]);
+                if (quad < NP) bc[l.ct][(t4 + (l.i >> 2)) * kWidth + (l.nb * 4 + l.row) * NP + quad] = v;
+                __builtin_amdgcn_sched_barrier(0);
             });
         });
 #pragma unroll
@@ -295,45 +328,80 @@ __global__ __launch_bounds__(64 * kWaves) void k_bwd(Args a) {
             da_lost[j] = (sum - da_all[j]) - v;
             da_all[j] = sum;
         }
-        __syncthreads();
-        // the four wavefronts' sums of b's and c's gradients
-        const int rows = min(F::kChunk, l.t_hi - t0);
-        const long long width = 2LL * a.G * a.N;
-        float* const to = a.part_bc + (((long long)tile * a.B + l.seq) * a.T + t0) * width + 2LL * l.group * a.N;
-        for (int k = threadIdx.x; k < F::kChunk * 2 * F::kStates; k += 64 * kWaves) {
-            const int m = k % F::kStates, which = k / F::kStates % 2, t = k / F::kStates / 2;
-            if (m >= a.N || t >= rows) continue;
-            float v = bc[0][t][which][m];
-            for (int w = 1; w < kWaves; ++w) v += bc[w][t][which][m];
-            to[t * width + which * a.N + m] = v;
+        lds_barrier();
+        // the workgroup's sums of b's and c's gradients
+        constexpr int kSums = kChunk * F::kStates * 2;
+#pragma unroll
+        for (int first_k = 0; first_k < kSums; first_k += F::kThreads) {
+            const int k = first_k + threadIdx.x, m = k % F::kStates, which = k / F::kStates % 2, t = k / (2 * F::kStates);
+            if (kSums % F::kThreads && k >= kSums) continue;
+            const float* const from = reinterpret_cast<const float*>(&bc[0][t * kWidth + m]) + which;
+            float v = from[0];
+#pragma unroll
+            for (int w = 1; w < F::CT; ++w) v += from[w * 2 * kChunk * kWidth];
+            if (full || t < n) part_[t * width + which * F::kStates + m] = v;
         }
-        __syncthreads();
+        part_ -= kChunk * width;
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            if ((q + 1) * F::kStep > 16 && !last_slot) continue;
+            const int t = first_t + F::kStep * q, at = t * F::kChannels + l.io_ch;
+            float gb = parts[0][0][at], qa = parts[1][0][at], ch = GATE ? parts[2][0][at] : 0.f;
+#pragma unroll
+            for (int k = 1; k < NB; ++k) {
+                gb += parts[0][k][at];
+                qa += parts[1][k][at];
+                if constexpr (GATE) ch += parts[2][k][at];
+            }
+            if (full || t < n) {
+                const float ddv = fmaf(xs[q], gb, kLn2 * qa) * slope[q];
+                gsc::store_one<D>(dx_.to(F::kStep * q), fmaf(skip, ds[q], delta[q] * gb));
+                gsc::store_one<D>(ddt_.to(F::kStep * q), ddv);
+                if constexpr (GATE) gsc::store_one<D>(dz_.to(F::kStep * q), dzf[q] * fmaf(skip, xs[q], ch));
+                dd = fmaf(ds[q], xs[q], dd);
+                dbias += ddv;
+            }
+        }
+        dx_.move(-kChunk);
+        ddt_.move(-kChunk);
+        if constexpr (GATE) dz_.move(-kChunk);
+    };
+    if (any) {
+        load(some, l.t_hi - t_last);
+        turn(some, l.t_hi - t_last, last > first);
+        loads_done();
+        for (int chunk = last - 1; chunk > first; --chunk) turn(whole, kChunk, true);
+        if (last > first) turn(some, kChunk, false);
     }
-    const long long at = ((long long)l.seq * a.S + l.s) * a.D + l.d;
-    const float sd = sum_rows(dd, dd, dd, dd), sbias = sum_rows(dbias, dbias, dbias, dbias);
+    // sums over positions
+    const long long at = ((long long)l.seq * a.S + l.s) * a.D;
+    const float sd = over_channel<F>(dd, reinterpret_cast<float*>(staged));
+    const float sbias = over_channel<F>(dbias, reinterpret_cast<float*>(staged));
+    if (threadIdx.x < F::kChannels) {
+        a.part_d[at + l.io_d] = sd;
+        a.part_bias[at + l.io_d] = sbias;
+    }
     if (!l.live) return;
 #pragma unroll
     for (int j = 0; j < NP; ++j)
         if (l.there[j]) {
-            a.part_a[at * a.N + l.row * NP + j] = da_all[j] * (kLn2 * l.a2[j]);
-            if (l.s == 0 && a.dh0) a.dh0[l.states_at + l.row * NP + j] = r[j];
+            a.part_a[(at + l.d) * a.N + l.at[j]] = da_all[j] * (kLn2 * l.a2[j]);
+            if (l.s == 0 && a.dh0) a.dh0[l.states_at + l.at[j]] = r[j];
         }
-    if (l.row == 0) {
-        a.part_d[at] = sd;
-        a.part_bias[at] = sbias;
-    }
 }
 
-// db and dc from the partial sums of the tiles of 64 channels, in order.
+// db and dc from the partial sums of the workgroups along the channels, in order; the
+// sums have `states` places for N.
 template <class D>
-__global__ __launch_bounds__(256) void k_close_bc(Args a) {
+__global__ __launch_bounds__(256) void k_close_bc(Args a, int states) {
     using S = typename D::S;
-    const int width = 2 * a.G * a.N;
+    const int width = 2 * a.G * states;
     const long long count = (long long)a.B * a.T * width;
     for (long long k = (long long)blockIdx.x * 256 + threadIdx.x; k < count; k += 256LL * gridDim.x) {
         const long long row = k / width;
         const int at = int(k % width), seq = int(row / a.T), t = int(row % a.T);
-        const int group = at / (2 * a.N), which = at / a.N % 2, m = at % a.N;
+        const int group = at / (2 * states), which = at / states % 2, m = at % states;
+        if (m >= a.N) continue;
         float v = 0.f;
         if (!a.lengths || t < a.lengths[seq])
             for (int j = 0; j < a.tiles; ++j) v += a.part_bc[j * count + k];
@@ -362,31 +430,20 @@ hipError_t close_par(const Args& a, int P, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <class D, int NP>
+template <class D, class F>
 hipError_t run_bwd(const Args& a, hipStream_t st) {
-    const dim3 block(64 * kWaves);
     const unsigned units = unsigned(a.G) * a.tiles * a.B * a.S;
     if (a.z) {
-        if (a.S > 1) k_back<D, NP, true><<<units, block, 0, st>>>(a);
-        k_bwd<D, NP, true><<<units, block, 0, st>>>(a);
+        if (a.S > 1) k_back<D, F, true><<<units, F::kThreads, 0, st>>>(a);
+        k_bwd<D, F, true><<<units, F::kThreads, 0, st>>>(a);
     } else {
-        if (a.S > 1) k_back<D, NP, false><<<units, block, 0, st>>>(a);
-        k_bwd<D, NP, false><<<units, block, 0, st>>>(a);
+        if (a.S > 1) k_back<D, F, false><<<units, F::kThreads, 0, st>>>(a);
+        k_bwd<D, F, false><<<units, F::kThreads, 0, st>>>(a);
     }
-    const long long count = (long long)a.B * a.T * 2 * a.G * a.N;
+    const long long count = (long long)a.B * a.T * 2 * a.G * F::kStates;
     const long long blocks = std::min((count + 255) / 256, 1LL << 16);
-    if (blocks) k_close_bc<D><<<unsigned(blocks), 256, 0, st>>>(a);
+    if (blocks) k_close_bc<D><<<unsigned(blocks), 256, 0, st>>>(a, F::kStates);
     return close_par(a, a.B * a.S, st);
-}
-template <class D>
-hipError_t run_bwd(const Args& a, int per_lane, hipStream_t st) {
-    switch (per_lane) {
-        case 1: return run_bwd<D, 1>(a, st);
-        case 2: return run_bwd<D, 2>(a, st);
-        case 4: return run_bwd<D, 4>(a, st);
-        case 8: return run_bwd<D, 8>(a, st);
-        default: return run_bwd<D, 16>(a, st);
-    }
 }
 
 }  // namespace
@@ -397,6 +454,7 @@ hipError_t bwd(const sscan_shape& s, Args a, void* ws, hipStream_t st) {
     const Plan p = plan(s, true);
     a.S = p.S;
     a.seg = p.seg;
+    a.tiles = p.tiles;
     const size_t rows = size_t(s.B) * s.D, all = rows * s.N;
     float* at = static_cast<float*>(ws);
     a.part_a = at;
@@ -406,14 +464,10 @@ hipError_t bwd(const sscan_shape& s, Args a, void* ws, hipStream_t st) {
     a.part_bias = at;
     at += p.S * rows;
     a.part_bc = at;
-    at += size_t(a.tiles) * s.B * s.T * s.G * 2 * s.N;
+    at += size_t(a.tiles) * s.B * s.T * s.G * 2 * (4 * p.per_lane * p.waves);
     a.seg_state = at;
     a.seg_sum = at + p.S * all;
-    switch (s.dtype) {
-        case GSCAN_F32: return run_bwd<F32>(a, p.per_lane, st);
-        case GSCAN_F16: return run_bwd<F16>(a, p.per_lane, st);
-        default: return run_bwd<BF16>(a, p.per_lane, st);
-    }
+    return with_form(s.dtype, p, [&](auto D, auto F) { return run_bwd<decltype(D), decltype(F)>(a, st); });
 }
 
 }  // namespace ssc

@@ -8,182 +8,219 @@
 namespace ssc {
 namespace {
 
-constexpr int kTile = 16;   // positions whose b and c a wavefront holds
-constexpr int kWaves = 4;   // of a workgroup: 64 channels, a cache line of 16-bit elements
-constexpr int kPad = 18;    // floats2 between two channels' rows in LDS: no bank conflicts
-
-// What a wavefront reads of a tile: each lane the elements of its channel at
-// every fourth position, and its row's states of one position.
-template <class D, int NP, bool GATE, bool SUMS>
-struct Tile {
-    float x[4], dt[4], z[4], b[NP], c[NP];
-    __device__ __forceinline__ void load(const Args& a, const typename D::S* x_, const typename D::S* dt_,
-                                         const typename D::S* z_, const typename D::S* b_,
-                                         const typename D::S* c_, int t0, int n, int row, int i,
-                                         bool whole) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const long long t = min(t0 + 4 * k + row, n - 1);
-            x[k] = gsc::load_one<D>(x_ + t * a.x_sr);
-            dt[k] = gsc::load_one<D>(dt_ + t * a.dt_sr);
-            if constexpr (GATE && SUMS) z[k] = gsc::load_one<D>(z_ + t * a.z_sr);
-        }
-        const bool valid = t0 + i < n;
-        const long long t = min(t0 + i, n - 1);
-        load_states<D, NP>(b, b_ + t * a.b_sr, row * NP, a.N, whole, valid);
-        if constexpr (SUMS) load_states<D, NP>(c, c_ + t * a.c_sr, row * NP, a.N, whole, valid);
-    }
-};
+constexpr int kPad = 18;  // float2s between two channels' rows in LDS: no bank conflicts
 
 // SUMS: the pass that gives y.  Otherwise: what a segment does to a state that
 // starts from zero, and its sum of delta (with which the state it starts from decays).
-template <class D, int NP, bool GATE, bool SUMS>
-__global__ __launch_bounds__(64 * kWaves) void k_fwd(Args a) {
+//
+// In a tile's turn the wavefronts compute from the delta and u in one half of LDS,
+// then put those of the next tile into the other half, and, past the barrier,
+// add up each other's sums over states and write y.
+template <class D, class F, bool GATE, bool SUMS>
+__global__ __launch_bounds__(F::kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))) void k_fwd(Args a) {
     using S = typename D::S;
-    __shared__ float2 lds[kWaves][16 * kPad];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = lane >> 4, i = lane & 15;
-    const int tiles = a.G * a.tiles;
-    const int tile = blockIdx.x % tiles, rest = blockIdx.x / tiles;
-    const int seq = rest / a.S, s = rest % a.S;
-    const int group = tile / a.tiles, c0 = (tile % a.tiles) * 64 + wave * 16;
-    if (c0 >= a.Dg) return;
-    const bool live = c0 + i < a.Dg;
-    const int d = group * a.Dg + min(c0 + i, a.Dg - 1);
-    const int n = a.lengths ? min(max(a.lengths[seq], 0), a.T) : a.T;
-    const int t_lo = s * a.seg, t_end = min(a.T - t_lo, a.seg) + t_lo, t_hi = min(t_end, n);
-    S* const y_ = SUMS ? (S*)a.y + seq * a.y_sb + d : nullptr;
-    const long long states_at = ((long long)seq * a.D + d) * a.N;  // of a [B][D][N]
-    const long long all = (long long)a.B * a.D * a.N;
+    constexpr int NP = F::NP, NB = F::NB, kSlots = F::kSlots;
+    __shared__ float2 staged[2][F::kChannels * kPad];
+    __shared__ float parts[2][SUMS ? NB : 1][SUMS ? 16 * F::kChannels : 1];
+    const Lane<F> l(a);
+    const int first_t = l.io_base + l.io_row;  // the thread's first position of a tile
+    const bool last_slot = l.last_slot;
 
     if constexpr (SUMS) {
-        if (live)
-            for (int t = max(n, t_lo) + row; t < t_end; t += 4)
-                gsc::store_one<D>(y_ + t * a.y_sr, 0.f);
+        if (max(l.n, l.t_lo) < l.t_end) {  // zeros behind the sequence
+            S* const y0 = (S*)a.y + l.seq * a.y_sb + l.io_d;
+            for (int t = max(l.n, l.t_lo) + first_t; t < l.t_end; t += F::kStep) gsc::store_one<D>(y0 + t * a.y_sr, 0.f);
+        }
     }
-    if (t_lo >= t_hi && !(SUMS && s == 0)) return;
-    if (!SUMS && s == a.S - 1) return;  // nothing starts from the last one's
+    if (l.t_lo >= l.t_hi && !(SUMS && l.s == 0)) return;
+    if (!SUMS && l.s == a.S - 1) return;  // nothing starts from the last one's
 
-    float a2[NP], h[NP];
-    bool there[NP];
+    float h[NP];
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int m = row * NP + j;
-        there[j] = m < a.N;
-        const int at = min(m, a.N - 1);
-        a2[j] = there[j] ? -kLog2e * expf(a.a_log[(long long)d * a.N + at]) : 0.f;
-        h[j] = SUMS && a.h0 && there[j] ? a.h0[states_at + at] : 0.f;
-    }
+    for (int j = 0; j < NP; ++j) h[j] = SUMS && a.h0 ? a.h0[l.states_at + l.at[j]] : 0.f;
+    auto keep = [&](float* to) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) to[l.states_at + l.at[j]] = h[j];
+    };
     if constexpr (SUMS) {
         // the segments before, one after the other
-        for (int k = 0; k < s; ++k) {
-            const float sum = a.seg_sum[((long long)k * a.B + seq) * a.D + d];
+        for (int k = 0; k < l.s; ++k) {
+            const float sum = a.seg_sum[((long long)k * a.B + l.seq) * a.D + l.d];
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const float own = a.seg_state[k * all + states_at + min(row * NP + j, a.N - 1)];
-                h[j] = there[j] ? fmaf(exp2_hw(sum * a2[j]), h[j], own) : 0.f;
-            }
+            for (int j = 0; j < NP; ++j)
+                h[j] = fmaf(exp2_hw(sum * l.a2[j]), h[j], a.seg_state[k * l.all + l.states_at + l.at[j]]);
         }
-        if (n == 0) {
-            if (live && a.h_last)
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-                    if (there[j]) a.h_last[states_at + row * NP + j] = h[j];
+        if (l.n == 0) {
+            if (a.h_last) keep(a.h_last);
             return;
         }
     }
-    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    const float skip = SUMS && a.d ? a.d[d] : 0.f;
-    const S* const x_ = (const S*)a.x + seq * a.x_sb + d;
-    const S* const dt_ = (const S*)a.dt + seq * a.dt_sb + d;
-    const S* const z_ = GATE && SUMS ? (const S*)a.z + seq * a.z_sb + d : nullptr;
-    const S* const b_ = (const S*)a.b + seq * a.b_sb + group * a.N;
-    const S* const c_ = SUMS ? (const S*)a.c + seq * a.c_sb + group * a.N : nullptr;
-    const bool whole = a.N == 4 * NP;
-    constexpr int kChunk = NP == 16 ? 16 : 32;
-    float2* const mine = lds[wave] + i * kPad;
+    const float skip = SUMS && a.d ? a.d[l.io_d] : 0.f;
+    auto wide = [&](const void* p, long long sb, long long sr) {
+        return Rows<S>(p, sb, sr, l.seq, l.t_lo + l.io_base, l.d0, l.io_row, l.io_ch);
+    };
+    Rows<S> x_ = wide(a.x, a.x_sb, a.x_sr), dt_ = wide(a.dt, a.dt_sb, a.dt_sr), z_ = wide(a.z, a.z_sb, a.z_sr);
+    Rows<S> y_ = wide(a.y, a.y_sb, a.y_sr);
+    const int low0 = l.group * a.N;
+    Rows<S> b_(a.b, a.b_sb, a.b_sr, l.seq, l.t_lo, low0, l.i, 0), c_(a.c, a.c_sb, a.c_sr, l.seq, l.t_lo, low0, l.i, 0);
+    float* states_ = SUMS && a.states ? a.states + saved_at(a, l, l.t_lo / kChunk) : nullptr;
+    const long long states_step = saved_at(a, l, 1) - saved_at(a, l, 0);
     float sum = 0.f;
 
-    Tile<D, NP, GATE, SUMS> now, next;
-    now.load(a, x_, dt_, z_, b_, c_, t_lo, n, row, i, whole);
-    for (int t0 = t_lo; t0 < t_hi; t0 += kTile) {
-        if (SUMS && a.states && t0 % kChunk == 0 && live) {
-            float* to = a.states + (t0 / kChunk) * all + states_at;
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-                if (there[j]) to[row * NP + j] = h[j];
-        }
-        float xs[4], zs[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const bool valid = t0 + 4 * k + row < t_hi && live;
-            xs[k] = now.x[k];
-            if constexpr (GATE && SUMS) zs[k] = now.z[k];
-            const float delta = valid ? softplus(now.dt[k] + bias).delta : 0.f;
-            if constexpr (!SUMS) sum += delta;
-            mine[4 * k + row] = make_float2(delta, valid ? delta * xs[k] : 0.f);
-        }
-        wave_sync();
-        if (t0 + kTile < t_hi) next.load(a, x_, dt_, z_, b_, c_, t0 + kTile, n, row, i, whole);
-        float own[4];
-        unroll<4>([&](auto K) {
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
-            unroll<4>([&](auto L) {
-                constexpr int k = 4 * K + L;
-                const float2 q = mine[k];
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    h[j] = fmaf(decay(q.x, a2[j]), h[j], bcast<k>(now.b[j]) * q.y);
-                    if constexpr (SUMS) part[L] = fmaf(bcast<k>(now.c[j]), h[j], part[L]);
-                }
-            });
-            if constexpr (SUMS) own[K] = sum_rows(part[0], part[1], part[2], part[3]);
-        });
-        if constexpr (SUMS) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = t0 + 4 * k + row;
-                float v = fmaf(skip, xs[k], own[k]);
-                if constexpr (GATE) v *= zs[k] * sig(zs[k]);
-                if (t < t_hi && live) gsc::store_one<D>(y_ + t * a.y_sr, v);
+    // What is read of a tile, `left` positions of which there are (`full`: all).
+    // Behind the sequence nothing is read.
+    Column<D, F> x, dt, z;
+    States<D, NP> b, c;
+    auto load = [&](auto full, int left) {
+        if constexpr (full) {
+            x.load(x_, last_slot);
+            dt.load(dt_, last_slot);
+            if constexpr (GATE && SUMS) z.load(z_, last_slot);
+            b.load(b_.at(0), l);
+            if constexpr (SUMS) c.load(c_.at(0), l);
+        } else {
+            x.load_some(x_, last_slot, left - first_t);
+            dt.load_some(dt_, last_slot, left - first_t);
+            if constexpr (GATE && SUMS) z.load_some(z_, last_slot, left - first_t);
+            b.clear();
+            c.clear();
+            if (l.i < left) {
+                b.load(b_.at(0), l);
+                if constexpr (SUMS) c.load(c_.at(0), l);
             }
         }
-        wave_sync();
-        now = next;
-    }
-    if (!live) return;
+        x_.move(kChunk);
+        dt_.move(kChunk);
+        b_.move(kChunk);
+        if constexpr (GATE && SUMS) z_.move(kChunk);
+        if constexpr (SUMS) c_.move(kChunk);
+    };
+    float xs[kSlots], zs[kSlots], bs[NP], cs[NP];
+    auto stage = [&](auto full, float2* to, int left) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            bs[j] = b[j];
+            now(bs[j]);
+            if constexpr (SUMS) {
+                cs[j] = l.there[j] ? c[j] : 0.f;
+                now(cs[j]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            if ((q + 1) * F::kStep > 16 && !last_slot) continue;
+            const int t = first_t + F::kStep * q;
+            const bool valid = full || t < left;
+            xs[q] = x[q];
+            now(xs[q]);
+            if constexpr (GATE && SUMS) {
+                zs[q] = z[q];
+                now(zs[q]);
+            }
+            const float delta = valid ? softplus(dt[q] + l.bias).delta : 0.f;
+            if constexpr (!SUMS) sum += delta;
+            to[l.io_at * kPad + t] = make_float2(delta, valid ? delta * xs[q] : 0.f);
+        }
+    };
+    int half = 0;
+    // One tile's turn.  full: it and the two that follow are whole, so that what is in flight
+    // at each point is known, and nothing is waited for before it is used.
+    auto turn = [&](auto full, int left) {
+        if (states_) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) states_[64 * j] = h[j];
+            states_ += states_step;
+        }
+        // Four positions at a time: while the states pass them, what the next four need is
+        // formed (their decays and inputs do not wait for the states), and those after
+        // that are on their way from LDS.
+        const float2* const mine = staged[half] + (l.ct * 16 + l.i) * kPad;
+        float2 m[2][4];
+        float e[2][4][NP], in[2][4][NP];
+        auto fetch = [&](auto K) {
+            constexpr int k = K;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m[k & 1][q] = mine[4 * k + q];
+        };
+        auto form = [&](auto K) {
+            constexpr int k = K;
+            unroll<4>([&](auto L) {
+                constexpr int q = L;
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    e[k & 1][q][j] = decay(m[k & 1][q].x, l.a2[j]);
+                    in[k & 1][q][j] = bcast<4 * k + q>(bs[j]) * m[k & 1][q].y;
+                }
+            });
+        };
+        fetch(std::integral_constant<int, 0>{});
+        fetch(std::integral_constant<int, 1>{});
+        form(std::integral_constant<int, 0>{});
+        unroll<4>([&](auto K) {
+            constexpr int k = K;
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (k < 2) fetch(std::integral_constant<int, k + 2>{});
+            float part[4];
+            unroll<4>([&](auto L) {
+                constexpr int q = L;
+#pragma unroll
+                for (int j = 0; j < NP; ++j) h[j] = fmaf(e[k & 1][q][j], h[j], in[k & 1][q][j]);
+                if constexpr (SUMS) part[q] = sum_bcast<4 * k + q>(cs, h);
+            });
+            if constexpr (k < 3) form(std::integral_constant<int, k + 1>{});
+            if constexpr (SUMS) parts[half][l.nb][(4 * k + l.row) * F::kChannels + l.ct * 16 + l.i] = sum_rows(part[0], part[1], part[2], part[3]);
+        });
+        float xe[kSlots], ze[kSlots];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            xe[q] = xs[q];
+            if constexpr (GATE && SUMS) ze[q] = zs[q];
+        }
+        if (full || left > kChunk) stage(full, staged[half ^ 1], left - kChunk);
+        if (full || left > 2 * kChunk) load(full, left - 2 * kChunk);
+        lds_barrier();
+        if constexpr (SUMS) {
+#pragma unroll
+            for (int q = 0; q < kSlots; ++q) {
+                if ((q + 1) * F::kStep > 16 && !last_slot) continue;
+                const int t = first_t + F::kStep * q;
+                float v = parts[half][0][t * F::kChannels + l.io_at];
+#pragma unroll
+                for (int k = 1; k < NB; ++k) v += parts[half][k][t * F::kChannels + l.io_at];
+                v = fmaf(skip, xe[q], v);
+                if constexpr (GATE) v *= ze[q] * sig(ze[q]);
+                if (full || t < left) gsc::store_one<D>(y_.to(F::kStep * q), v);
+            }
+            y_.move(kChunk);
+        }
+        half ^= 1;
+    };
+    constexpr std::true_type whole{};
+    constexpr std::false_type some{};
+    int left = l.t_hi - l.t_lo;
+    load(some, left);
+    stage(some, staged[0], left);
+    if (left > kChunk) load(some, left - kChunk);
+    lds_barrier();
+    loads_done();
+    for (; left >= 3 * kChunk; left -= kChunk) turn(whole, left);
+    for (; left > 0; left -= kChunk) turn(some, left);
     if constexpr (SUMS) {
-        if (a.h_last && t_hi == n)
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-                if (there[j]) a.h_last[states_at + row * NP + j] = h[j];
+        if (a.h_last && l.t_hi == l.n) keep(a.h_last);
     } else {
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-            if (there[j]) a.seg_state[s * all + states_at + row * NP + j] = h[j];
-        const float total = sum_rows(sum, sum, sum, sum);
-        if (row == 0) a.seg_sum[((long long)s * a.B + seq) * a.D + d] = total;
+        keep(a.seg_state + l.s * l.all);
+        const float total = over_channel<F>(sum, reinterpret_cast<float*>(staged));
+        if (threadIdx.x < F::kChannels) a.seg_sum[((long long)l.s * a.B + l.seq) * a.D + l.io_d] = total;
     }
 }
 
-template <class D, int NP>
+template <class D, class F>
 hipError_t run_fwd(const Args& a, hipStream_t st) {
-    const dim3 block(64 * kWaves);
     const unsigned units = unsigned(a.G) * a.tiles * a.B * a.S;
-    if (a.S > 1) k_fwd<D, NP, false, false><<<units, block, 0, st>>>(a);
-    if (a.z) k_fwd<D, NP, true, true><<<units, block, 0, st>>>(a);
-    else k_fwd<D, NP, false, true><<<units, block, 0, st>>>(a);
+    if (a.S > 1) k_fwd<D, F, false, false><<<units, F::kThreads, 0, st>>>(a);
+    if (a.z) k_fwd<D, F, true, true><<<units, F::kThreads, 0, st>>>(a);
+    else k_fwd<D, F, false, true><<<units, F::kThreads, 0, st>>>(a);
     return hipGetLastError();
-}
-template <class D>
-hipError_t run_fwd(const Args& a, int per_lane, hipStream_t st) {
-    switch (per_lane) {
-        case 1: return run_fwd<D, 1>(a, st);
-        case 2: return run_fwd<D, 2>(a, st);
-        case 4: return run_fwd<D, 4>(a, st);
-        case 8: return run_fwd<D, 8>(a, st);
-        default: return run_fwd<D, 16>(a, st);
-    }
 }
 
 // One position: four lanes per channel, each with every fourth group of V states.
@@ -248,23 +285,28 @@ hipError_t run_step(const StepArgs& a, hipStream_t st) {
 Plan plan(const sscan_shape& s, bool backward) {
     Plan p{};
     const int q = (s.N + 3) / 4;
-    p.per_lane = q <= 1 ? 1 : q <= 2 ? 2 : q <= 4 ? 4 : q <= 8 ? 8 : 16;
-    p.chunk = p.per_lane == 16 ? 16 : 32;
-    const long long tiles = s.G ? (s.D / s.G + 63) / 64 : 0;
-    const long long units = s.G * tiles * s.B;
-    const long long chunks = (s.T + p.chunk - 1LL) / p.chunk;
-    p.fits = units < (1LL << 20) && s.B * ((s.T + 15LL) / 16) < (1LL << 31);
-    // workgroups enough for two on each compute unit, segments of 4 chunks at least
+    p.per_lane = q <= 1 ? 1 : q <= 8 ? 2 : 4;
+    p.waves = (q + p.per_lane - 1) / p.per_lane;
+    p.width = p.waves <= 2 ? 64 : 32;
+    p.tiles = s.G ? (s.D / s.G + p.width - 1) / p.width : 0;
+    const long long units = (long long)s.G * p.tiles * s.B;
+    const long long chunks = (s.T + kChunk - 1LL) / kChunk;
+    p.fits = units < (1LL << 20) && s.B * chunks < (1LL << 31);
+    // One workgroup on a compute unit takes 88 ns a position forwards and 246 backwards (16 states),
+    // however many others there are up to 256; a second one on it costs 30% more for both.
+    // Segments cost a pass over all but the last more.  4096 positions of 2048 channels, bf16:
+    // 8 sequences (256 workgroups) 351 us forwards whole, 430 in 4 segments; 6 (192) 361 and 510 in 2,
+    // 377 in 5; 4 (128) 361 and 263 in 4; 1 (32) 361 and 87 in 8 or 16, 110 in 32.
     long long S = 1;
-    if (units && units < 256) S = std::max(1LL, std::min({512 / units, chunks / 4, 64LL}));
-    const long long per = S ? (chunks + S - 1) / S : 0;
-    p.seg = int(std::max(1LL, per) * p.chunk);
+    if (units && units < 192) S = std::max(1LL, std::min({512 / units, chunks / 8, 64LL}));
+    const long long per = (chunks + S - 1) / S;
+    p.seg = int(std::max(1LL, per) * kChunk);
     p.S = int(std::max(1LL, per ? (chunks + per - 1) / per : 1));
     const size_t rows = size_t(s.B) * s.D, all = rows * s.N;
-    p.states = 4 * size_t(chunks) * all;
+    p.states = 4 * size_t(chunks) * units * p.width * (4 * p.per_lane * p.waves);
     if (p.S > 1) p.scratch += 4 * size_t(p.S) * (all + rows);
     if (backward) {
-        p.scratch += 4 * size_t(tiles) * s.B * s.T * s.G * 2 * s.N;
+        p.scratch += 4 * size_t(p.tiles) * s.B * s.T * s.G * 2 * (4 * p.per_lane * p.waves);
         p.scratch += 4 * size_t(p.S) * (all + 2 * rows);
     }
     return p;
@@ -274,13 +316,10 @@ hipError_t fwd(const sscan_shape& s, Args a, void* ws, hipStream_t st) {
     const Plan p = plan(s, false);
     a.S = p.S;
     a.seg = p.seg;
+    a.tiles = p.tiles;
     a.seg_state = static_cast<float*>(ws);
     a.seg_sum = a.seg_state + size_t(p.S) * s.B * s.D * s.N;
-    switch (s.dtype) {
-        case GSCAN_F32: return run_fwd<F32>(a, p.per_lane, st);
-        case GSCAN_F16: return run_fwd<F16>(a, p.per_lane, st);
-        default: return run_fwd<BF16>(a, p.per_lane, st);
-    }
+    return with_form(s.dtype, p, [&](auto D, auto F) { return run_fwd<decltype(D), decltype(F)>(a, st); });
 }
 
 hipError_t step(int dtype, const StepArgs& a, hipStream_t st) {

@@ -10,6 +10,8 @@
 
 namespace ssc {
 
+constexpr int kChunk = 16;  // positions between two saved states
+
 // One call, as the kernels take it.
 struct Args {
     const void *x, *dt, *b, *c, *z, *dy;
@@ -25,13 +27,14 @@ struct Args {
     float* part_bc;  // [tiles of a group][B][T][G][2][N]
     float *part_a, *part_d, *part_bias;  // [B * S][D][N], [B * S][D] twice
     int B, T, D, N, G;
-    int Dg, tiles;  // channels of a group, and tiles of 64 of them
+    int Dg, tiles;  // channels of a group, and workgroups for them
     int S, seg;
 };
 
 struct Plan {
-    int per_lane;      // states that a lane holds: 1, 2, 4, 8 or 16
-    int chunk;         // positions between two saved states
+    int per_lane;      // states that a lane holds: 1, 2 or 4
+    int waves;         // wavefronts that the states of 16 channels are divided among
+    int width, tiles;  // channels of a workgroup, and workgroups for a group's
     int S, seg;        // segments of a sequence, and their length
     size_t states;     // bytes
     size_t scratch;    // bytes of workspace

@@ -71,11 +71,11 @@ typedef struct {
  * Sizes: B * D and D * N up to 2^25, B * D * N up to 2^31, G * N up to 2^20
  * (WTCONV_ERR_SHAPE beyond).  What one launch does not hold is refused with
  * WTCONV_ERR_UNSUPPORTED: G * ceil(D / G / 64) * B has to be below 2^20, and
- * B * ceil(T / 16) below 2^31.
+ * B * ceil(T / 16) below 2^31; and so are strides of a position above 2^26.
  */
 
-/* Bytes of the states sscan_fwd writes for sscan_bwd: h before each piece of
- * 16 to 64 positions. */
+/* Bytes of the states sscan_fwd writes for sscan_bwd: h before each 16
+ * positions. */
 int sscan_states_size(const sscan_shape* s, size_t* bytes);
 
 /* Bytes of device workspace that sscan_fwd, and with `backward` sscan_bwd, needs. */
