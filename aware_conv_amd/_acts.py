@@ -41,19 +41,11 @@ def read(out, x, groups, flats):
     groups: (names, tensors); the tensors of a group are of one shape and dtype, the first's, and
     the others may be None.  flats: (name, tensor, dtype, dims, optional), contiguous.  All are on
     x's device."""
-    at = first = ctypes.addressof(out)
-    device = x.device.index
-    bad = False
-    for _, tensors in groups:
-        if tensors[0] is not None:
-            bad = bad or _lists.views(tensors, at) >= 0 or tensors[0].device != x.device
-        at += VIEW * len(tensors)
-    if not bad:
-        ps = [_lists.flat(t, dtype, device, *(n if len(n) > 1 else (n[0], -1))) for _, t, dtype, n, _ in flats]
-        bad = any(p is False or (p is None and not f[4]) for p, f in zip(ps, flats))
-    if bad:
+    at = ctypes.addressof(out)
+    ps = _lists.read(at, x, groups, flats)
+    if ps is None:
         _refuse(x, groups, flats)
-    return first, ps
+    return at, ps
 
 
 def _refuse(x, groups, flats):

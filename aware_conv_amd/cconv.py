@@ -20,6 +20,12 @@ _Views2, _Views3 = _lib.GscanView * 2, _lib.GscanView * 3
 
 
 @functools.lru_cache(maxsize=256)
+def _form(*shape):
+    """The shape as the library takes it; it is only read."""
+    return ctypes.byref(_lib.CconvShape(*shape))
+
+
+@functools.lru_cache(maxsize=256)
 def _need(*shape):
     """Bytes of the backward's workspace for a shape."""
     s, n = _lib.CconvShape(*shape), ctypes.c_size_t(0)
@@ -61,7 +67,7 @@ def cconv_fwd(x, w, bias=None, h0=None, lengths=None, silu=True, y=None, *, stre
         y = torch.empty(x.shape, dtype=x.dtype, device=dev)
         v[1] = _view(y)
     last = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
-    _lib._enqueue(dev, "cconv_fwd", ctypes.byref(_lib.CconvShape(*shape)), p, pw, pb, ph0, plen, p + VIEW,
+    _lib._enqueue(dev, "cconv_fwd", _form(*shape), p, pw, pb, ph0, plen, p + VIEW,
                   last.data_ptr(), _raw_stream(stream, dev))
     if given is not None:
         _lists.written(given)
@@ -98,7 +104,7 @@ def cconv_bwd(x, w, dy, bias=None, h0=None, dlast=None, lengths=None, silu=True,
             at = grads[n].data_ptr()
         out.append(at)
     ws, pws, nws = _acts.workspace(_need(*shape), dev, workspace)
-    _lib._enqueue(dev, "cconv_bwd", ctypes.byref(_lib.CconvShape(*shape)), p, pw, pb, ph0, plen, p + VIEW, plast,
+    _lib._enqueue(dev, "cconv_bwd", _form(*shape), p, pw, pb, ph0, plen, p + VIEW, plast,
                   p + 2 * VIEW, out[0], out[1], out[2], pws, nws, _raw_stream(stream, dev))
     _lists.written(given)
     return {n: grads.get(n) for n in GRAD_NAMES}
@@ -122,7 +128,7 @@ def cconv_step(x, w, cache, bias=None, slots=None, silu=True, y=None, *, stream=
     if y is None:
         y = torch.empty((B, C), dtype=x.dtype, device=dev)
         v[1] = _view(y)
-    _lib._enqueue(dev, "cconv_step", ctypes.byref(_lib.CconvShape(*shape)), S, p, pw, pb, pcache, pslots, p + VIEW,
+    _lib._enqueue(dev, "cconv_step", _form(*shape), S, p, pw, pb, pcache, pslots, p + VIEW,
                   _raw_stream(stream, dev))
     _lists.written(cache, given)
     return y

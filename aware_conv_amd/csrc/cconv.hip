@@ -46,7 +46,7 @@ __device__ __forceinline__ void load(float (&out)[V], const typename D::S* p, in
 template <class D, int V>
 __device__ __forceinline__ void store(typename D::S* p, const float (&v)[V], int left) {
     if (left >= V) {
-        gsc::store_vec<D, V>(p, gsc::pack<D, false>(v));
+        gsc::store_vec_once<D, V>(p, gsc::pack<D, false>(v));
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -328,9 +328,7 @@ hipError_t bwd(const cconv_shape& s, Args a, void* ws, hipStream_t st) {
         if (e != hipSuccess) return e;
     }
     const long long nw = (long long)a.C * a.K;
-    const hipError_t e = calls::close_sums<1>(a.part, parts, nw, nw, a.dw, st);
-    if (e != hipSuccess || !a.dbias) return e;
-    return calls::close_sums<1>(a.part + parts * nw, parts, a.C, a.C, a.dbias, st);
+    return calls::close_sums<1>(parts, st, {a.part, nw, a.dw}, {a.part + parts * nw, a.C, a.dbias});
 }
 
 hipError_t step(int dtype, const StepArgs& a, hipStream_t st) {

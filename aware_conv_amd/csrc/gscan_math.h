@@ -116,6 +116,22 @@ __device__ __forceinline__ void store_vec(typename D::S* p, const Raw<D, V>& v) 
     for (int k = 0; k < Raw<D, V>::kWords; ++k) q.w[k] = v.w[k];
     *reinterpret_cast<P*>(p) = q;
 }
+// The same for what a kernel writes and nobody reads soon: past the caches' order of use.
+template <class D, int V>
+__device__ __forceinline__ void store_vec_once(typename D::S* p, const Raw<D, V>& v) {
+    constexpr int kWords = Raw<D, V>::kWords, kPiece = kWords < 4 ? kWords : 4;
+    static_assert(kWords % kPiece == 0 && kPiece != 3, "whole vectors");
+    typedef uint32_t W1 __attribute__((aligned(2)));
+    typedef uint32_t W2 __attribute__((ext_vector_type(2), aligned(2)));
+    typedef uint32_t W4 __attribute__((ext_vector_type(4), aligned(2)));
+    using W = std::conditional_t<kPiece == 1, W1, std::conditional_t<kPiece == 2, W2, W4>>;
+#pragma unroll
+    for (int k = 0; k < kWords; k += kPiece) {
+        W q;
+        __builtin_memcpy(&q, v.w + k, 4 * kPiece);
+        __builtin_nontemporal_store(q, reinterpret_cast<W*>(p) + k / kPiece);
+    }
+}
 template <class D>
 __device__ __forceinline__ float load_one(const typename D::S* p) {
     if constexpr (D::kBytes == 4) return *p;

@@ -21,7 +21,7 @@ using gsc::F32;
 
 constexpr int kV = 8;             // elements of a vector
 constexpr float kTop = 448.f;     // the largest e4m3 value
-constexpr unsigned kParts = 512;  // workgroups of the backward pass at most
+constexpr unsigned kParts = 1024;  // workgroups of the backward pass at most
 
 // Elements c..c + 7 of a row of C, zero beyond it.
 template <class D>
@@ -39,7 +39,7 @@ __device__ __forceinline__ void load(float (&v)[kV], const typename D::S* p, int
 template <class D>
 __device__ __forceinline__ void store(typename D::S* p, const float (&v)[kV], int c, int C) {
     if (c + kV <= C) {
-        gsc::store_vec<D, kV>(p + c, gsc::pack<D, false>(v));
+        gsc::store_vec_once<D, kV>(p + c, gsc::pack<D, false>(v));
     } else {
 #pragma unroll
         for (int j = 0; j < kV; ++j)
@@ -392,7 +392,7 @@ hipError_t bwd(const rmsnorm_shape& s, Args a, void* ws, hipStream_t st) {
         });
         if (e != hipSuccess) return e;
     }
-    return a.dw ? calls::close_sums<2>(a.part, p.parts, a.C, a.C, a.dw, st) : hipSuccess;
+    return calls::close_sums<2>(p.parts, st, {a.part, a.C, a.dw});
 }
 
 }  // namespace rmn

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 
+#include "close_sums.h"
 #include "sscan_math.h"
 
 namespace ssc {
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(F::kThreads) __attribute__((amdgpu_waves_per_eu(2, 
             }
         }
 #pragma unroll
-        for (int j = 0; j < NP; ++j) saved[j] = states_[64 * j];
+        for (int j = 0; j < NP; ++j) saved[j] = __builtin_nontemporal_load(states_ + 64 * j);
         x_.move(-kChunk);
         dt_.move(-kChunk);
         dy_.move(-kChunk);
@@ -402,32 +403,24 @@ __global__ __launch_bounds__(256) void k_close_bc(Args a, int states) {
         const int at = int(k % width), seq = int(row / a.T), t = int(row % a.T);
         const int group = at / (2 * states), which = at / states % 2, m = at % states;
         if (m >= a.N) continue;
-        float v = 0.f;
-        if (!a.lengths || t < a.lengths[seq])
-            for (int j = 0; j < a.tiles; ++j) v += a.part_bc[j * count + k];
+        float v[4] = {};
+        if (!a.lengths || t < a.lengths[seq]) {
+            const float* const from = a.part_bc + k;
+            int j = 0;
+            for (; j + 3 < a.tiles; j += 4)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += from[(j + q) * count];
+            for (; j < a.tiles; ++j) v[0] += from[j * count];
+        }
         S* const to = which ? (S*)a.dc + seq * a.dc_sb + t * a.dc_sr : (S*)a.db + seq * a.db_sb + t * a.db_sr;
-        gsc::store_one<D>(to + group * a.N + m, v);
+        gsc::store_one<D>(to + group * a.N + m, (v[0] + v[1]) + (v[2] + v[3]));
     }
 }
 
-// The parameters' gradients from P partial sums each, added in order in fp64.
-__global__ __launch_bounds__(256) void k_close_par(Args a, int P) {
-    const long long k = (long long)blockIdx.x * 256 + threadIdx.x, na = (long long)a.D * a.N;
-    if (k >= na + 2 * a.D) return;
-    const bool of_a = k < na, of_d = !of_a && k - na < a.D;
-    const float* const from = of_a ? a.part_a + k : of_d ? a.part_d + (k - na) : a.part_bias + (k - na - a.D);
-    float* const to = of_a ? a.da_log + k : of_d ? a.dd + (k - na) : a.ddt_bias + (k - na - a.D);
-    if (!of_a && !(of_d ? a.dd : a.ddt_bias)) return;
-    const long long step = of_a ? na : a.D;
-    double v = 0;
-    for (int p = 0; p < P; ++p) v += from[p * step];
-    *to = float(v);
-}
-
-hipError_t close_par(const Args& a, int P, hipStream_t st) {
-    const long long n = (long long)a.D * a.N + 2LL * a.D;
-    k_close_par<<<unsigned((n + 255) / 256), 256, 0, st>>>(a, P);
-    return hipGetLastError();
+// The parameters' gradients from P partial sums each.
+hipError_t close_par(const Args& a, long long P, hipStream_t st) {
+    return calls::close_sums<3>(P, st, {a.part_a, (long long)a.D * a.N, a.da_log}, {a.part_d, a.D, a.dd},
+                                {a.part_bias, a.D, a.ddt_bias});
 }
 
 template <class D, class F>
@@ -443,7 +436,7 @@ hipError_t run_bwd(const Args& a, hipStream_t st) {
     const long long count = (long long)a.B * a.T * 2 * a.G * F::kStates;
     const long long blocks = std::min((count + 255) / 256, 1LL << 16);
     if (blocks) k_close_bc<D><<<unsigned(blocks), 256, 0, st>>>(a, F::kStates);
-    return close_par(a, a.B * a.S, st);
+    return close_par(a, (long long)a.B * a.S, st);
 }
 
 }  // namespace

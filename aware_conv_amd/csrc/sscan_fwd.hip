@@ -128,7 +128,7 @@ __global__ __launch_bounds__(F::kThreads) __attribute__((amdgpu_waves_per_eu(2, 
     auto turn = [&](auto full, int left) {
         if (states_) {
 #pragma unroll
-            for (int j = 0; j < NP; ++j) states_[64 * j] = h[j];
+            for (int j = 0; j < NP; ++j) __builtin_nontemporal_store(h[j], states_ + 64 * j);
             states_ += states_step;
         }
         // Four positions at a time: while the states pass them, what the next four need is
@@ -223,61 +223,88 @@ hipError_t run_fwd(const Args& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// One position: four lanes per channel, each with every fourth group of V states.
-template <class D, int V>
+// One position.  The states are most of what is read and written; four lanes take a
+// channel, V of its states at a time, of Q sequences, so that Q vectors of states
+// are under way in each thread and a channel's rates are formed once for all of them.
+template <class D, int V, int Q>
 __global__ __launch_bounds__(256) void k_step(StepArgs a) {
     using S = typename D::S;
-    const long long at = (long long)blockIdx.x * 64 + threadIdx.x / 4;
-    const int q = threadIdx.x & 3;
-    if (at >= (long long)a.B * a.D) return;
-    const int seq = int(at / a.D), d = int(at % a.D), group = d / a.Dg;
-    const int slot = a.slots ? a.slots[seq] : seq;
-    S* const y = (S*)a.y + seq * a.y_sb + d;
-    if (slot < 0 || slot >= a.S) {
-        if (q == 0) gsc::store_one<D>(y, 0.f);
-        return;
+    const int per = (a.D + 63) / 64, seq0 = blockIdx.x / per * Q;
+    const int d = blockIdx.x % per * 64 + threadIdx.x / 4, lane = threadIdx.x & 3, group = d / a.Dg;
+    if (d >= a.D) return;  // whole groups of four
+    float x[Q], delta[Q], sum[Q];
+    float* h_[Q];
+    const S *b_[Q], *c_[Q];
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int seq = min(seq0 + q, a.B - 1);
+        const int slot = a.slots ? a.slots[seq] : seq;
+        const bool on = seq0 + q < a.B && slot >= 0 && slot < a.S;
+        h_[q] = on ? a.state + ((long long)slot * a.D + d) * a.N : nullptr;
+        b_[q] = (const S*)a.b + seq * a.b_sb + group * a.N;
+        c_[q] = (const S*)a.c + seq * a.c_sb + group * a.N;
+        x[q] = gsc::load_one<D>((const S*)a.x + seq * a.x_sb + d);
+        delta[q] = gsc::load_one<D>((const S*)a.dt + seq * a.dt_sb + d);
+        sum[q] = 0.f;
     }
-    const float x = gsc::load_one<D>((const S*)a.x + seq * a.x_sb + d);
-    const float pre = gsc::load_one<D>((const S*)a.dt + seq * a.dt_sb + d) + (a.dt_bias ? a.dt_bias[d] : 0.f);
-    const float delta = softplus(pre).delta, u = delta * x;
-    float* const h_ = a.state + ((long long)slot * a.D + d) * a.N;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) delta[q] = softplus(delta[q] + bias).delta;
     const float* const a_ = a.a_log + (long long)d * a.N;
-    const S* const b_ = (const S*)a.b + seq * a.b_sb + group * a.N;
-    const S* const c_ = (const S*)a.c + seq * a.c_sb + group * a.N;
-    float sum = 0.f;
-    for (int m = q * V; m < a.N; m += 4 * V) {
-        float h[V], al[V];
-        gsc::Raw<F32, V> r;
-        gsc::load_vec<F32, V>(r, h_ + m);
+    for (int m = lane * V; m < a.N; m += 4 * V) {
+        gsc::Raw<F32, V> h[Q], al;
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[j] = r.get(j);
-        gsc::load_vec<F32, V>(r, a_ + m);
+        for (int q = 0; q < Q; ++q)
+            if (h_[q]) gsc::load_vec<F32, V>(h[q], h_[q] + m);
+        gsc::load_vec<F32, V>(al, a_ + m);
+        float b[Q][V], c[Q][V], a2[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) al[j] = r.get(j);
+        for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            h[j] = fmaf(decay(delta, -kLog2e * expf(al[j])), h[j], u * gsc::load_one<D>(b_ + m + j));
-            sum = fmaf(gsc::load_one<D>(c_ + m + j), h[j], sum);
+            for (int j = 0; j < V; ++j) {
+                b[q][j] = gsc::load_one<D>(b_[q] + m + j);
+                c[q][j] = gsc::load_one<D>(c_[q] + m + j);
+            }
+#pragma unroll
+        for (int j = 0; j < V; ++j) a2[j] = -kLog2e * expf(al.get(j));
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (!h_[q]) continue;
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] = fmaf(decay(delta[q], a2[j]), h[q].get(j), delta[q] * x[q] * b[q][j]);
+                sum[q] = fmaf(c[q][j], v[j], sum[q]);
+            }
+            gsc::store_vec<F32, V>(h_[q] + m, gsc::pack<F32, false>(v));
         }
-        gsc::store_vec<F32, V>(h_ + m, gsc::pack<F32, false>(h));
     }
-    sum += __shfl_xor(sum, 1);
-    sum += __shfl_xor(sum, 2);
-    if (q) return;
-    if (a.d) sum = fmaf(a.d[d], x, sum);
-    if (a.z) {
-        const float z = gsc::load_one<D>((const S*)a.z + seq * a.z_sb + d);
-        sum *= z * sig(z);
+    const float skip = a.d ? a.d[d] : 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        sum[q] += __shfl_xor(sum[q], 1);
+        sum[q] += __shfl_xor(sum[q], 2);
+        if (lane || seq0 + q >= a.B) continue;
+        float v = fmaf(skip, x[q], sum[q]);
+        if (a.z) {
+            const float z = gsc::load_one<D>((const S*)a.z + (seq0 + q) * a.z_sb + d);
+            v *= z * sig(z);
+        }
+        gsc::store_one<D>((S*)a.y + (seq0 + q) * a.y_sb + d, h_[q] ? v : 0.f);
     }
-    gsc::store_one<D>(y, sum);
 }
 
+template <class D, int V>
+hipError_t run_step(const StepArgs& a, hipStream_t st) {
+    const long long per = (a.D + 63) / 64;
+    // four sequences to a thread where that leaves workgroups for all compute units
+    if (a.B * per >= 4096) k_step<D, V, 4><<<unsigned((a.B + 3) / 4 * per), 256, 0, st>>>(a);
+    else k_step<D, V, 1><<<unsigned(a.B * per), 256, 0, st>>>(a);
+    return hipGetLastError();
+}
 template <class D>
 hipError_t run_step(const StepArgs& a, hipStream_t st) {
-    const unsigned blocks = unsigned(((long long)a.B * a.D + 63) / 64);
-    if (a.N % 4 == 0) k_step<D, 4><<<blocks, 256, 0, st>>>(a);
-    else k_step<D, 1><<<blocks, 256, 0, st>>>(a);
-    return hipGetLastError();
+    return a.N % 4 == 0 ? run_step<D, 4>(a, st) : run_step<D, 1>(a, st);
 }
 
 }  // namespace

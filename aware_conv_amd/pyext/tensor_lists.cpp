@@ -130,24 +130,97 @@ PyObject* views(PyObject* args) {
     return PyLong_FromLong(-1);
 }
 
-// flat(tensor, dtype, device, n0, n1[, n2]) -> address, None for None, False if
-// it does not fit: contiguous, of that dtype on that CUDA device, of the shape
-// (n0, n1, n2), (n0, n1) without n2, or (n0,) for a negative n1.
+// flat(tensor, dtype, device, n0, n1) -> address, None for None, False if it
+// does not fit: contiguous, of that dtype on that CUDA device, of the shape
+// (n0, n1), or (n0,) for a negative n1.
 PyObject* flat(PyObject* args) {
     PyObject *o, *dtype;
     int device;
-    long long n0, n1, n2 = -1;
-    if (!PyArg_ParseTuple(args, "OOiLL|L", &o, &dtype, &device, &n0, &n1, &n2)) return nullptr;
+    long long n0, n1;
+    if (!PyArg_ParseTuple(args, "OOiLL", &o, &dtype, &device, &n0, &n1)) return nullptr;
     if (o == Py_None) Py_RETURN_NONE;
     if (!THPVariable_Check(o) || !THPDtype_Check(dtype)) Py_RETURN_FALSE;
     const at::Tensor& t = THPVariable_Unpack(o);
-    const int dims = n1 < 0 ? 1 : n2 < 0 ? 2 : 3;
+    const int dims = n1 < 0 ? 1 : 2;
     if (t.scalar_type() != reinterpret_cast<THPDtype*>(dtype)->scalar_type || !t.is_cuda() ||
         t.device().index() != device || t.layout() != at::kStrided || t.dim() != dims ||
-        t.size(0) != n0 || (dims > 1 && t.size(1) != n1) || (dims > 2 && t.size(2) != n2) ||
-        !t.is_contiguous())
+        t.size(0) != n0 || (dims == 2 && t.size(1) != n1) || !t.is_contiguous())
         Py_RETURN_FALSE;
     return PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.data_ptr()));
+}
+
+// read(address, x, groups, flats) -> list of addresses, or None where something does
+// not fit.
+//
+// groups: a tuple of (names, tensors), each tensors a tuple as views takes it, whose
+// first may be None too, and then the rest is not looked at; their views are written
+// one after the other.  flats: a tuple of (name, tensor, dtype, sizes, optional), each
+// tensor as flat takes it, with None for None where that is allowed.  Everything is on
+// x's device.
+PyObject* read(PyObject* args) {
+    unsigned long long address;
+    PyObject *xo, *groups, *flats;
+    if (!PyArg_ParseTuple(args, "KOO!O!", &address, &xo, &PyTuple_Type, &groups, &PyTuple_Type, &flats))
+        return nullptr;
+    if (!THPVariable_Check(xo)) Py_RETURN_NONE;
+    const auto device = THPVariable_Unpack(xo).device();
+    if (!device.is_cuda()) Py_RETURN_NONE;
+    long long* out = reinterpret_cast<long long*>(address);
+    for (Py_ssize_t g = 0; g < PyTuple_GET_SIZE(groups); ++g) {
+        PyObject* pair = PyTuple_GET_ITEM(groups, g);
+        if (!PyTuple_Check(pair) || PyTuple_GET_SIZE(pair) != 2 || !PyTuple_Check(PyTuple_GET_ITEM(pair, 1))) {
+            PyErr_SetString(PyExc_ValueError, "read: bad arguments");
+            return nullptr;
+        }
+        PyObject* tuple = PyTuple_GET_ITEM(pair, 1);
+        const Py_ssize_t n = PyTuple_GET_SIZE(tuple);
+        const at::Tensor* first = nullptr;
+        for (Py_ssize_t i = 0; i < n; ++i, out += 3) {
+            PyObject* o = PyTuple_GET_ITEM(tuple, i);
+            out[0] = out[1] = out[2] = 0;
+            if (o == Py_None || (i > 0 && !first)) continue;
+            if (!THPVariable_Check(o)) Py_RETURN_NONE;
+            const at::Tensor& t = THPVariable_Unpack(o);
+            if (i == 0) first = &t;
+            if (t.device() != device || t.layout() != at::kStrided || t.dim() < 2 || t.dim() > 4 ||
+                t.scalar_type() != first->scalar_type() || t.sizes() != first->sizes() || !adjacent(t))
+                Py_RETURN_NONE;
+            out[0] = reinterpret_cast<long long>(t.data_ptr());
+            out[1] = t.stride(0);
+            out[2] = t.stride(1);
+        }
+    }
+    const Py_ssize_t count = PyTuple_GET_SIZE(flats);
+    PyObject* list = PyList_New(count);
+    if (!list) return nullptr;
+    for (Py_ssize_t k = 0; k < count; ++k) {
+        PyObject* f = PyTuple_GET_ITEM(flats, k);
+        bool fits = PyTuple_Check(f) && PyTuple_GET_SIZE(f) == 5 && PyTuple_Check(PyTuple_GET_ITEM(f, 3));
+        PyObject* at = nullptr;
+        if (fits) {
+            PyObject *o = PyTuple_GET_ITEM(f, 1), *dtype = PyTuple_GET_ITEM(f, 2), *sizes = PyTuple_GET_ITEM(f, 3);
+            if (o == Py_None) {
+                fits = PyTuple_GET_ITEM(f, 4) == Py_True;
+                Py_INCREF(Py_None);
+                at = Py_None;
+            } else if ((fits = THPVariable_Check(o) && THPDtype_Check(dtype))) {
+                const at::Tensor& t = THPVariable_Unpack(o);
+                fits = t.scalar_type() == reinterpret_cast<THPDtype*>(dtype)->scalar_type && t.device() == device &&
+                       t.layout() == at::kStrided && t.dim() == PyTuple_GET_SIZE(sizes) && t.is_contiguous();
+                for (int64_t a = 0; fits && a < t.dim(); ++a)
+                    fits = t.size(a) == PyLong_AsLongLong(PyTuple_GET_ITEM(sizes, a));
+                if (fits) at = PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.data_ptr()));
+            }
+        }
+        if (!fits || !at) {
+            Py_XDECREF(at);
+            Py_DECREF(list);
+            if (PyErr_Occurred()) return nullptr;
+            Py_RETURN_NONE;
+        }
+        PyList_SET_ITEM(list, k, at);
+    }
+    return list;
 }
 
 // written(tensors...) -- advances the version counters of what a call has
@@ -171,6 +244,7 @@ PyObject* written(PyObject* args) {
 }
 
 PyMethodDef methods[] = {{"views", guarded<views>, METH_VARARGS, "Checks strided activations and writes their views."},
+                         {"read", guarded<read>, METH_VARARGS, "Checks activations and contiguous tensors of a call."},
                          {"flat", guarded<flat>, METH_VARARGS, "Checks a contiguous tensor and returns its address."},
                          {"column", guarded<column>, METH_VARARGS, "Checks a list of tensors and writes their addresses."},
                          {"written", guarded<written>, METH_VARARGS, "Advances tensors' version counters."},

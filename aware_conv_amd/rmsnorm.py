@@ -19,6 +19,12 @@ _Views4, _Views5 = _lib.GscanView * 4, _lib.GscanView * 5
 
 
 @functools.lru_cache(maxsize=256)
+def _form(*shape):
+    """The shape as the library takes it; it is only read."""
+    return ctypes.byref(_lib.RmsnormShape(*shape))
+
+
+@functools.lru_cache(maxsize=256)
 def _need(*shape):
     """Bytes of the backward's workspace for a shape."""
     s, n = _lib.RmsnormShape(*shape), ctypes.c_size_t(0)
@@ -62,11 +68,10 @@ def _forward(x, w, residual, eps, y, total, scale, save_rstd, stream, e4m3):
         raise ValueError("total is given without a residual")
     rcode = code if residual is None else _stream_code(x, code, "residual", residual)
     v = _Views4()  # x, y, residual, total
-    groups = [(("x", "y"), (x, None if e4m3 else y)), (("residual", "total"), (residual, total))]
-    flats = [("w", w, f32, (C,), False)]
-    if e4m3:
-        flats.append(("scale", scale, f32, tuple(x.shape[:-1]), True))
-    p, ps = _acts.read(v, x, groups, flats)
+    rows = x.shape[:-1]
+    p, (pw, pscale) = _acts.read(
+        v, x, ((("x", "y"), (x, None if e4m3 else y)), (("residual", "total"), (residual, total))),
+        (("w", w, f32, (C,), False), ("scale", scale, f32, rows, True)))
     dev = x.device
     given = [t for t in (y, total, scale) if t is not None]
     if e4m3 and y is not None:
@@ -77,20 +82,18 @@ def _forward(x, w, residual, eps, y, total, scale, save_rstd, stream, e4m3):
         _put(v, 1, y)
     if y is None:
         y = torch.empty(x.shape, dtype=torch.float8_e4m3fn if e4m3 else x.dtype, device=dev)
-        _put(v, 1, y)
+        v[1] = y.data_ptr(), T * C, C
     if residual is not None and total is None:
         total = torch.empty(x.shape, dtype=residual.dtype, device=dev)
-        _put(v, 3, total)
+        v[3] = total.data_ptr(), T * C, C
     if e4m3 and scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=f32, device=dev)
-    rstd = torch.empty(x.shape[:-1], dtype=f32, device=dev) if save_rstd else None
+        scale = torch.empty(rows, dtype=f32, device=dev)
+        pscale = scale.data_ptr()
+    rstd = torch.empty(rows, dtype=f32, device=dev) if save_rstd else None
     there = residual is not None
-    args = [ctypes.byref(_lib.RmsnormShape(B, T, C, code, rcode, eps)), p, p + 2 * VIEW if there else None, ps[0],
-            p + VIEW]
-    if e4m3:
-        args.append(scale.data_ptr())
-    _lib._enqueue(dev, "rmsnorm_fwd_e4m3" if e4m3 else "rmsnorm_fwd", *args, p + 3 * VIEW if there else None,
-                  None if rstd is None else rstd.data_ptr(), _raw_stream(stream, dev))
+    args = (p, p + 2 * VIEW if there else None, pw, p + VIEW, *((pscale,) if e4m3 else ()),
+            p + 3 * VIEW if there else None, None if rstd is None else rstd.data_ptr(), _raw_stream(stream, dev))
+    _lib._enqueue(dev, "rmsnorm_fwd_e4m3" if e4m3 else "rmsnorm_fwd", _form(B, T, C, code, rcode, eps), *args)
     if given:
         _lists.written(given)
     return y, total, scale, rstd
@@ -130,7 +133,7 @@ def rmsnorm_bwd(kept, w, rstd, dy, dtotal=None, grads=None, workspace=None, *, s
     p, (pw, prstd, pdw) = _acts.read(
         v, dy, ((("dy", "grads[dx]"), (dy, get("dx"))),
                 (("kept", "dtotal", "grads[dresidual]"), (kept, dtotal, get("dresidual")))),
-        (("w", w, f32, (C,), False), ("rstd", rstd, f32, tuple(dy.shape[:-1]), False),
+        (("w", w, f32, (C,), False), ("rstd", rstd, f32, dy.shape[:-1], False),
          ("grads[dw]", get("dw"), f32, (C,), True)))
     dev = dy.device
     if get("dx") is None:
@@ -143,7 +146,7 @@ def rmsnorm_bwd(kept, w, rstd, dy, dtotal=None, grads=None, workspace=None, *, s
         grads["dw"] = torch.empty(C, dtype=f32, device=dev)
         pdw = grads["dw"].data_ptr()
     ws, pws, nws = _acts.workspace(_need(B, T, C, code, rcode, 0.0), dev, workspace)
-    _lib._enqueue(dev, "rmsnorm_bwd", ctypes.byref(_lib.RmsnormShape(B, T, C, code, rcode, 0.0)), p + 2 * VIEW, pw,
+    _lib._enqueue(dev, "rmsnorm_bwd", _form(B, T, C, code, rcode, 0.0), p + 2 * VIEW, pw,
                   prstd, p, None if dtotal is None else p + 3 * VIEW, p + VIEW, p + 4 * VIEW if two else None, pdw,
                   pws, nws, _raw_stream(stream, dev))
     _lists.written(given)

@@ -19,6 +19,12 @@ _Views6, _Views11 = _lib.GscanView * 6, _lib.GscanView * 11
 
 
 @functools.lru_cache(maxsize=256)
+def _form(*shape):
+    """The shape as the library takes it; it is only read."""
+    return ctypes.byref(_lib.SscanShape(*shape))
+
+
+@functools.lru_cache(maxsize=256)
 def _sizes(*shape):
     """(floats of the states, bytes of the forward's workspace, of the backward's) for a shape."""
     s, n = _lib.SscanShape(*shape), ctypes.c_size_t(0)
@@ -79,7 +85,7 @@ def sscan_fwd(x, dt, a_log, b, c, d=None, z=None, dt_bias=None, h0=None, lengths
     n_states, need, _ = _sizes(*shape)
     states = torch.empty(n_states, dtype=f32, device=dev) if save_states else None
     ws, pws, nws = _acts.workspace(need, dev, workspace)
-    _lib._enqueue(dev, "sscan_fwd", ctypes.byref(_lib.SscanShape(*shape)), p, p + VIEW, pa, p + 4 * VIEW,
+    _lib._enqueue(dev, "sscan_fwd", _form(*shape), p, p + VIEW, pa, p + 4 * VIEW,
                   p + 5 * VIEW, pd, None if z is None else p + 2 * VIEW, pbias, ph0, plen, p + 3 * VIEW,
                   h_last.data_ptr(), None if states is None else states.data_ptr(), pws, nws,
                   _raw_stream(stream, dev))
@@ -127,7 +133,7 @@ def sscan_bwd(x, dt, a_log, b, c, states, dy, d=None, z=None, dt_bias=None, dh_l
             at = grads[n].data_ptr()
         out.append(at)
     ws, pws, nws = _acts.workspace(need, dev, workspace)
-    _lib._enqueue(dev, "sscan_bwd", ctypes.byref(_lib.SscanShape(*shape)), p, p + VIEW, pa, p + 7 * VIEW,
+    _lib._enqueue(dev, "sscan_bwd", _form(*shape), p, p + VIEW, pa, p + 7 * VIEW,
                   p + 8 * VIEW, pd, None if z is None else p + 2 * VIEW, pbias, pst, plen, p + 3 * VIEW, plast,
                   p + 4 * VIEW, p + 5 * VIEW, out[0], p + 9 * VIEW, p + 10 * VIEW, out[1],
                   None if z is None else p + 6 * VIEW, out[2], out[3], pws, nws, _raw_stream(stream, dev))
@@ -155,7 +161,7 @@ def sscan_step(x, dt, a_log, b, c, state, d=None, z=None, dt_bias=None, slots=No
     if y is None:
         y = torch.empty((B, D), dtype=x.dtype, device=dev)
         v[3] = _view(y)
-    _lib._enqueue(dev, "sscan_step", ctypes.byref(_lib.SscanShape(*shape)), S, p, p + VIEW, pa, p + 4 * VIEW,
+    _lib._enqueue(dev, "sscan_step", _form(*shape), S, p, p + VIEW, pa, p + 4 * VIEW,
                   p + 5 * VIEW, pd, None if z is None else p + 2 * VIEW, pbias, pstate, pslots, p + 3 * VIEW,
                   _raw_stream(stream, dev))
     _lists.written(state, given)
