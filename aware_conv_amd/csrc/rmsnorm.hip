@@ -23,6 +23,8 @@ constexpr int kV = 8;             // elements of a vector
 constexpr float kTop = 448.f;     // the largest e4m3 value
 constexpr unsigned kParts = 1024;  // workgroups of the backward pass at most
 
+constexpr long long kBlocks = 1 << 21;  // of the forward pass: a launch has fewer than 2^32 threads
+
 // Elements c..c + 7 of a row of C, zero beyond it.
 template <class D>
 __device__ __forceinline__ void load(float (&v)[kV], const typename D::S* p, int c, int C) {
@@ -96,118 +98,123 @@ template <class D, class R, int THREADS, int NV, bool E4M3>
 __global__ __launch_bounds__(kBlock<THREADS>) void k_fwd(Args a) {
     __shared__ float lds[16];
     const int tid = threadIdx.x % THREADS;
-    const long long row = (long long)blockIdx.x * (kBlock<THREADS> / THREADS) + threadIdx.x / THREADS;
-    if (row >= a.rows) return;  // whole wavefronts, and with THREADS > 64 none
-    const long long b = row / a.T, t = row % a.T;
-    const typename D::S* const x = (const typename D::S*)a.x + b * a.x_sb + t * a.x_sr;
-    const typename R::S* const res = (const typename R::S*)a.res + b * a.res_sb + t * a.res_sr;
-    typename R::S* const total = (typename R::S*)a.total + b * a.total_sb + t * a.total_sr;
-    const bool add = a.res != nullptr;
-    const int C = a.C;
-    constexpr int kStep = THREADS * kV;
+    constexpr int kRows = kBlock<THREADS> / THREADS;
+    const long long first_row = (long long)blockIdx.x * kRows + threadIdx.x / THREADS;
+    // one turn, unless there are more rows than a launch has threads for; rows of more than a
+    // wavefront have a workgroup of their own, whose threads take the same turns
+    for (long long row = first_row; row < a.rows; row += (long long)gridDim.x * kRows) {
+        const long long b = row / a.T, t = row % a.T;
+        const typename D::S* const x = (const typename D::S*)a.x + b * a.x_sb + t * a.x_sr;
+        const typename R::S* const res = (const typename R::S*)a.res + b * a.res_sb + t * a.res_sr;
+        typename R::S* const total = (typename R::S*)a.total + b * a.total_sb + t * a.total_sr;
+        const bool add = a.res != nullptr;
+        const int C = a.C;
+        constexpr int kStep = THREADS * kV;
 
-    auto first = [&](float(&v)[kV], int c) {  // s, and its share of the sum of squares
-        load<D>(v, x, c, C);
-        if (add) {
-            float r[kV];
-            load<R>(r, res, c, C);
+        auto first = [&](float(&v)[kV], int c) {  // s, and its share of the sum of squares
+            load<D>(v, x, c, C);
+            if (add) {
+                float r[kV];
+                load<R>(r, res, c, C);
 #pragma unroll
-            for (int j = 0; j < kV; ++j) v[j] = rounded<R>(v[j] + r[j]);
-            store<R>(total, v, c, C);
+                for (int j = 0; j < kV; ++j) v[j] = rounded<R>(v[j] + r[j]);
+                store<R>(total, v, c, C);
+            }
+            float q = 0.f;
+#pragma unroll
+            for (int j = 0; j < kV; ++j) q = fmaf(v[j], v[j], q);
+            return q;
+        };
+        float s[NV ? NV : 1][kV], sum = 0.f;
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = k * kStep + tid * kV;
+                if (c < C) {
+                    sum += first(s[k], c);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) s[k][j] = 0.f;
+                }
+            }
+        } else {
+            for (int c = tid * kV; c < C; c += kStep) sum += first(s[0], c);
         }
-        float q = 0.f;
+        sum = over_row<THREADS, false>(sum, lds);
+        const float rstd = 1.f / sqrtf(sum / float(C) + a.eps);
+        if (a.rstd && tid == 0) a.rstd[row] = rstd;
+
+        auto normed = [&](float(&v)[kV], int c) {
+            float w[kV];
+            load<F32>(w, a.w, c, C);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) q = fmaf(v[j], v[j], q);
-        return q;
-    };
-    float s[NV ? NV : 1][kV], sum = 0.f;
-    if constexpr (NV > 0) {
+            for (int j = 0; j < kV; ++j) v[j] = v[j] * rstd * w[j];
+        };
+        auto again = [&](float(&v)[kV], int c) {
+            if (add) load<R>(v, total, c, C);
+            else load<D>(v, x, c, C);
+            normed(v, c);
+        };
+        if constexpr (!E4M3) {
+            typename D::S* const y = (typename D::S*)a.y + b * a.y_sb + t * a.y_sr;
+            if constexpr (NV > 0) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = k * kStep + tid * kV;
-            if (c < C) {
-                sum += first(s[k], c);
+                for (int k = 0; k < NV; ++k) {
+                    const int c = k * kStep + tid * kV;
+                    if (c >= C) continue;
+                    normed(s[k], c);
+                    store<D>(y, s[k], c, C);
+                }
             } else {
-#pragma unroll
-                for (int j = 0; j < kV; ++j) s[k][j] = 0.f;
-            }
-        }
-    } else {
-        for (int c = tid * kV; c < C; c += kStep) sum += first(s[0], c);
-    }
-    sum = over_row<THREADS, false>(sum, lds);
-    const float rstd = 1.f / sqrtf(sum / float(C) + a.eps);
-    if (a.rstd && tid == 0) a.rstd[row] = rstd;
-
-    auto normed = [&](float(&v)[kV], int c) {
-        float w[kV];
-        load<F32>(w, a.w, c, C);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) v[j] = v[j] * rstd * w[j];
-    };
-    auto again = [&](float(&v)[kV], int c) {
-        if (add) load<R>(v, total, c, C);
-        else load<D>(v, x, c, C);
-        normed(v, c);
-    };
-    if constexpr (!E4M3) {
-        typename D::S* const y = (typename D::S*)a.y + b * a.y_sb + t * a.y_sr;
-        if constexpr (NV > 0) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = k * kStep + tid * kV;
-                if (c >= C) continue;
-                normed(s[k], c);
-                store<D>(y, s[k], c, C);
+                for (int c = tid * kV; c < C; c += kStep) {
+                    again(s[0], c);
+                    store<D>(y, s[0], c, C);
+                }
             }
         } else {
-            for (int c = tid * kV; c < C; c += kStep) {
-                again(s[0], c);
-                store<D>(y, s[0], c, C);
-            }
-        }
-    } else {
-        uint8_t* const y = (uint8_t*)a.y + b * a.y_sb + t * a.y_sr;
-        float top = 0.f;
-        auto most = [&](const float(&v)[kV]) {
+            uint8_t* const y = (uint8_t*)a.y + b * a.y_sb + t * a.y_sr;
+            float top = 0.f;
+            auto most = [&](const float(&v)[kV]) {
 #pragma unroll
-            for (int j = 0; j < kV; ++j) top = fmaxf(top, fabsf(v[j]));
-        };
-        if constexpr (NV > 0) {
+                for (int j = 0; j < kV; ++j) top = fmaxf(top, fabsf(v[j]));
+            };
+            if constexpr (NV > 0) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = k * kStep + tid * kV;
-                if (c >= C) continue;
-                normed(s[k], c);
-                most(s[k]);
+                for (int k = 0; k < NV; ++k) {
+                    const int c = k * kStep + tid * kV;
+                    if (c >= C) continue;
+                    normed(s[k], c);
+                    most(s[k]);
+                }
+            } else {
+                for (int c = tid * kV; c < C; c += kStep) {
+                    again(s[0], c);
+                    most(s[0]);
+                }
             }
-        } else {
-            for (int c = tid * kV; c < C; c += kStep) {
-                again(s[0], c);
-                most(s[0]);
-            }
-        }
-        top = over_row<THREADS, true>(top, lds);
-        const float scale = top / kTop, inv = scale > 0.f ? 1.f / scale : 0.f;
-        if (tid == 0) a.scale[row] = scale;
-        auto codes = [&](float(&v)[kV], int c) {
+            top = over_row<THREADS, true>(top, lds);
+            // below the normal numbers a scale has no inverse: such a row is zero
+            const float scale = top / kTop >= 1.17549435e-38f ? top / kTop : 0.f, inv = scale > 0.f ? 1.f / scale : 0.f;
+            if (tid == 0) a.scale[row] = scale;
+            auto codes = [&](float(&v)[kV], int c) {
 #pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                const float q = v[j] * inv;
-                v[j] = q > kTop ? kTop : q < -kTop ? -kTop : q;  // a NaN stays
-            }
-            store_codes(y, v, c, C);
-        };
-        if constexpr (NV > 0) {
+                for (int j = 0; j < kV; ++j) {
+                    const float q = v[j] * inv;
+                    v[j] = q > kTop ? kTop : q < -kTop ? -kTop : q;  // a NaN stays
+                }
+                store_codes(y, v, c, C);
+            };
+            if constexpr (NV > 0) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = k * kStep + tid * kV;
-                if (c < C) codes(s[k], c);
-            }
-        } else {
-            for (int c = tid * kV; c < C; c += kStep) {
-                again(s[0], c);
-                codes(s[0], c);
+                for (int k = 0; k < NV; ++k) {
+                    const int c = k * kStep + tid * kV;
+                    if (c < C) codes(s[k], c);
+                }
+            } else {
+                for (int c = tid * kV; c < C; c += kStep) {
+                    again(s[0], c);
+                    codes(s[0], c);
+                }
             }
         }
     }
@@ -363,7 +370,7 @@ Plan plan(const rmsnorm_shape& s) {
 
 hipError_t fwd(const rmsnorm_shape& s, const Args& a, bool e4m3, hipStream_t st) {
     const Plan p = plan(s);
-    const unsigned blocks = unsigned((a.rows + p.per_block - 1) / p.per_block);
+    const unsigned blocks = unsigned(std::min((a.rows + p.per_block - 1) / p.per_block, kBlocks));
     return with_types(s, [&](auto D, auto R) {
         return with_width(p, [&](auto W) {
             using T = decltype(D);

@@ -165,7 +165,6 @@ int sscan_bwd(const sscan_shape* s, const gscan_view* x, const gscan_view* dt, c
     q.flat(dh0, all, true, true);
     if (workspace && ws_bytes >= p.scratch) q.flat(workspace, (long long)p.scratch, true, true, 1);
     if ((rc = q.done())) return rc;
-    if (s->D == 0) return WTCONV_OK;
     ssc::Args a = args_of(*s);
     a.a_log = a_log;
     a.d = d;

@@ -426,7 +426,8 @@ hipError_t close_par(const Args& a, long long P, hipStream_t st) {
 template <class D, class F>
 hipError_t run_bwd(const Args& a, hipStream_t st) {
     const unsigned units = unsigned(a.G) * a.tiles * a.B * a.S;
-    if (a.z) {
+    if (units == 0) {  // no channels: the sums over them are zero
+    } else if (a.z) {
         if (a.S > 1) k_back<D, F, true><<<units, F::kThreads, 0, st>>>(a);
         k_bwd<D, F, true><<<units, F::kThreads, 0, st>>>(a);
     } else {

@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256) void k_step(StepArgs a) {
                 c[q][j] = gsc::load_one<D>(c_[q] + m + j);
             }
 #pragma unroll
-        for (int j = 0; j < V; ++j) a2[j] = -kLog2e * expf(al.get(j));
+        for (int j = 0; j < V; ++j) a2[j] = rate_of(al.get(j));
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             if (!h_[q]) continue;

@@ -39,6 +39,8 @@ using gsc::kLog2e;
 using gsc::rcp_hw;
 using gsc::sig;
 
+__device__ __forceinline__ float rate_of(float a_log);
+
 // Which wavefronts of a workgroup hold what.
 template <int NP_, int NB_>
 struct Form {
@@ -124,7 +126,7 @@ struct Lane {
             const int m = (nb * 4 + row) * NP + j;
             there[j] = m < a.N;
             at[j] = min(m, a.N - 1);
-            a2[j] = -gsc::kLog2e * expf(a.a_log[(long long)d * a.N + at[j]]);
+            a2[j] = rate_of(a.a_log[(long long)d * a.N + at[j]]);
         }
     }
 };
@@ -226,6 +228,11 @@ __device__ __forceinline__ float sum_rows(float v0, float v1, float v2, float v3
 // most 3e-10 down to 0.9993, 3e-9 down to 0.994, where a state forgets it
 // sooner: 1.2e-6 of a state at most.  The power of 1e-8 is 1.
 constexpr float kLift = 1e-8f;
+// A' from a_log; finite, so that a step of zero leaves a state as it is.
+__device__ __forceinline__ float rate_of(float a_log) {
+    const float v = -kLog2e * expf(a_log);
+    return v < -3e38f ? -3e38f : v;
+}
 __device__ __forceinline__ float decay(float delta, float a2) {
     return exp2_hw(fmaf(delta, a2, kLift));
 }

@@ -13,8 +13,8 @@
  *
  *   scale = max |y| / 448             codes = y / scale in e4m3, to nearest even
  *
- * (a row of zeros has scale 0 and codes 0; a NaN has the code NaN).  Gradients, for dy of y and
- * dtotal of `total`, with n = s rstd:
+ * (a row whose scale would be below 2^-126 has scale 0 and codes 0; a NaN has the
+ * code NaN).  Gradients, for dy of y and dtotal of `total`, with n = s rstd:
  *
  *   g = dy w       ds = rstd (g - n mean(g n)) + dtotal       dw = sum over rows of dy n
  *

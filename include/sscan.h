@@ -70,8 +70,9 @@ typedef struct {
 /*
  * Sizes: B * D and D * N up to 2^25, B * D * N up to 2^31, G * N up to 2^20
  * (WTCONV_ERR_SHAPE beyond).  What one launch does not hold is refused with
- * WTCONV_ERR_UNSUPPORTED: G * ceil(D / G / 64) * B has to be below 2^20, and
- * B * ceil(T / 16) below 2^31; and so are strides of a position above 2^26.
+ * WTCONV_ERR_UNSUPPORTED: G * ceil(D / G / 64) * B has to be below 2^20 (a 32 for
+ * the 64 where N > 16), and B * ceil(T / 16) below 2^31; and so are strides of a
+ * position above 2^26.
  */
 
 /* Bytes of the states sscan_fwd writes for sscan_bwd: h before each 16

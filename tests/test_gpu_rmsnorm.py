@@ -177,6 +177,52 @@ def test_sizes_of_values(scale):
     check(s, what=("size", scale))
 
 
+def test_more_rows_than_a_launch_has_threads_for():
+    import aware_conv_amd as A
+    n = (1 << 26) + 5
+    x = torch.ones(n, 1, dtype=torch.float16, device="cuda")
+    x[-3:, 0] = torch.tensor([2.0, 0.0, -3.0])
+    w = torch.full((1,), 0.5, device="cuda")
+    y, _, rstd = A.rmsnorm_fwd(x, w, eps=0.0, save_rstd=True)
+    assert (y[:-3] == 0.5).all() and (rstd[:-3] == 1).all()
+    assert y[-3:, 0].nan_to_num(9).tolist() == [0.5, 9.0, -0.5]  # a row of zeros without eps has no norm
+    dw = A.rmsnorm_bwd(x[:-3], w, rstd[:-3], y[:-3])["dw"]
+    # halves are added exactly, and their sum, 33554433, is rounded: fp32 has every fourth number there
+    assert dw.item() == torch.tensor((n - 3) * 0.5, dtype=torch.float32).item()
+
+
+@pytest.mark.parametrize("top", [1e-30, 1e-36, 2e-38, 1e-42, 0.0])
+def test_scales_of_small_rows(top):
+    """Down to where the scale leaves the normal numbers, and the row is zero."""
+    import aware_conv_amd as A
+    x = torch.ones(1, 1, 100, device="cuda")
+    x[0, 0, ::3] = 0
+    w = torch.full((100,), top, device="cuda")
+    q, scale, _ = A.rmsnorm_fwd_e4m3(x, w, eps=0.0)
+    y = A.rmsnorm_fwd(x, w, eps=0.0)[0]
+    assert torch.isfinite(q.float()).all()
+    if float(y.max()) / 448 >= 2.0 ** -126:
+        # the largest is coded as 448: what the scale rounds to is all that is off
+        assert ((q.double() * scale.double()[..., None] - y.double()).abs() <= 2.0 ** -22 * y.double()).all()
+    else:
+        assert scale.item() == 0 and (q.float() == 0).all()
+
+
+def test_into_a_product_in_8_bits():
+    """As it is used: codes and scales of rows into a product whose weights are coded by rows too.
+    Both are off by at most 2^-4 of each value, mean 2^-5.5 of either sign: 0.04 of the result's
+    size covers the sum of 256 such terms."""
+    import aware_conv_amd as A
+    s = make(1, 40, 256, "bf16", "f32", seed=1)
+    weight = torch.randn(512, 256, device="cuda")
+    size = weight.abs().amax(1, keepdim=True) / 448
+    codes = (weight / size).to(torch.float8_e4m3fn)
+    q, scale, total = A.rmsnorm_fwd_e4m3(s["x"], s["w"], residual=s["res"])
+    got = torch._scaled_mm(q[0], codes.t(), scale_a=scale[0][:, None], scale_b=size.t(), out_dtype=torch.bfloat16)
+    want = A.rmsnorm_fwd(s["x"].float(), s["w"], residual=s["res"])[0][0] @ weight.t()
+    assert (got.float() - want).norm() <= 0.04 * want.norm()
+
+
 def test_no_rows():
     import aware_conv_amd as A
     for B, T, C in ((0, 3, 20), (2, 0, 20), (2, 3, 0)):

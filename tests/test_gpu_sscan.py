@@ -218,6 +218,51 @@ def test_steps_of_any_size():
     check(s, what="any size")
 
 
+@pytest.mark.parametrize("lengths", [None, [37, 5, 0]])
+def test_rates_beyond_the_largest_number(lengths):
+    """exp(a_log) is infinite: such a state forgets everything at each step, and what is behind a
+    sequence leaves it as it is."""
+    import aware_conv_amd as A
+    s = make(3, 37, 18, 8, seed=6)
+    s["a_log"][:, 3] = 100.0
+    form = {k: s[k] for k in ("d", "z", "dt_bias")}
+    form["lengths"] = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    args = [s[k] for k in ("x", "dt", "a_log", "b", "c")]
+    y, h, states = A.sscan_fwd(*args, h0=s["h0"], save_states=True, **form)
+    g = A.sscan_bwd(*args, states, s["dy"], dh_last=s["dh_last"], **form)
+    for i, n in enumerate(ref.counts(3, 37, lengths)):
+        if n:  # the last step's input alone
+            t = n - 1
+            u = torch.nn.functional.softplus(s["dt"][i, t] + s["dt_bias"]) * s["x"][i, t]
+            assert (h[i, :, 3] - u * s["b"][i, t, 3]).abs().max() <= 1e-6 * h.abs().max()
+        else:
+            assert torch.equal(h[i], s["h0"][i])
+    assert torch.isfinite(y).all() and torch.isfinite(h).all()
+    for k in ("dx", "ddt", "dz", "db", "dc", "dd", "ddt_bias", "dh0", "da_log"):
+        assert torch.isfinite(g[k]).all(), k
+
+
+def test_no_channels():
+    """Sums over no channels are zero."""
+    import aware_conv_amd as A
+    z = lambda *n: torch.zeros(*n, device="cuda")  # noqa: E731
+    args = [z(2, 20, 0), z(2, 20, 0), z(0, 4), torch.randn(2, 20, 4, device="cuda"), torch.randn(2, 20, 4, device="cuda")]
+    y, h, states = A.sscan_fwd(*args, save_states=True)
+    low = torch.full((2, 20, 8), 7.0, device="cuda")
+    g = A.sscan_bwd(*args, states, y, grads={"db": low[..., :4], "dc": low[..., 4:]})
+    assert y.shape == (2, 20, 0) and h.shape == (2, 0, 4) and (low == 0).all() and g["da_log"].shape == (0, 4)
+
+
+def test_no_positions():
+    import aware_conv_amd as A
+    s = make(2, 0, 6, 4, seed=1)
+    args = [s[k] for k in ("x", "dt", "a_log", "b", "c")]
+    y, h, states = A.sscan_fwd(*args, h0=s["h0"], save_states=True)
+    g = A.sscan_bwd(*args, states, s["dy"], dh_last=s["dh_last"])
+    assert y.shape == (2, 0, 6) and torch.equal(h, s["h0"]) and torch.equal(g["dh0"], s["dh_last"])
+    assert (g["da_log"] == 0).all() and g["db"].shape == (2, 0, 4)
+
+
 def test_two_runs_agree_bit_for_bit():
     s = make(3, 900, 70, 16, dtype="bf16", seed=8)
     a, b = check(s, what="first"), check(s, what="second")
@@ -325,6 +370,32 @@ def test_positions_one_by_one(N):
     parts = [y] + [A.sscan_step(*args(t), cache, z=s["z"][:, t], **form)[:, None] for t in range(37, 60)]
     assert (torch.cat(parts, 1) - whole).abs().max() <= 1e-5 * whole.abs().max()
     assert (cache - last).abs().max() <= 1e-5 * last.abs().max()
+
+
+@pytest.mark.parametrize("B,D,N", [(40, 2100, 16), (9, 33000, 5)])
+def test_many_single_positions(B, D, N):
+    """So many that a thread takes several sequences; the last group of them is not whole."""
+    import aware_conv_amd as A
+    s = make(B, 1, D, N, dtype="bf16", seed=D)
+    S = B + 2
+    cache = torch.randn(S, D, N, device="cuda")
+    before = cache.clone()
+    slots = torch.randperm(S)[:B].to(torch.int32)
+    slots[3], slots[B - 1] = S, -7
+    form = {"d": s["d"], "dt_bias": s["dt_bias"]}
+    at = lambda t, i: t[i:i + 1, 0]  # noqa: E731
+    y = A.sscan_step(s["x"][:, 0], s["dt"][:, 0], s["a_log"], s["b"][:, 0], s["c"][:, 0], cache, z=s["z"][:, 0],
+                     slots=slots.cuda(), **form)
+    for i in range(B):
+        k = int(slots[i])
+        if not 0 <= k < S:
+            assert (y[i] == 0).all()
+            continue
+        one = before[k:k + 1].clone()
+        want = A.sscan_step(at(s["x"], i), at(s["dt"], i), s["a_log"], at(s["b"], i), at(s["c"], i), one, z=at(s["z"], i), **form)
+        assert torch.equal(y[i:i + 1], want) and torch.equal(cache[k], one[0])
+    rest = [k for k in range(S) if k not in slots.tolist()]
+    assert torch.equal(cache[rest], before[rest])
 
 
 # autograd ----------------------------------------------------------------------

@@ -3,13 +3,16 @@ any device call, and the tests' own fp64 reference.  CPU only: every call to the
 fails validation, or has nothing to do."""
 import copy
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import token_reference as ref
 from aware_conv_amd import _lib as L
-from aware_conv_amd import SelectiveMixer, cconv, rmsnorm, sscan
+from aware_conv_amd import SelectiveMixer, _acts, cconv, rmsnorm, sscan
 
 NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, UNSUPPORTED, ALIAS, LAYOUT, VALUE = -1, -2, -5, -6, -7, -8, -9, -11, -12
 
@@ -92,6 +95,15 @@ def test_scan_forward_arguments():
     e = sshape(B=0)
     none = L.GscanView(None, 0, 0)
     assert sfwd(e, x=none, dt=none, b=none, c=none, z=none, y=none, h0=None, h_last=None, states=None, ws=None) == 0
+
+
+def test_scan_strides():
+    """Fifteen rows of a stride are within 32 bits; a single position's stride does not matter."""
+    for n in ("x", "dt", "z"):
+        assert sfwd(**{n: wide(0, sr=(1 << 26) + 1), "y": wide(10)}, ws=None) == UNSUPPORTED, n
+    assert sfwd(b=low(3, sr=(1 << 26) + 1), y=wide(10), ws=None) == UNSUPPORTED
+    assert sfwd(y=wide(10, sb=1 << 33, sr=(1 << 26) + 1), ws=None) == UNSUPPORTED
+    assert sbwd(dx=wide(15, sb=1 << 33, sr=(1 << 26) + 1)) == UNSUPPORTED and sbwd(dx=wide(15, sb=1 << 33, sr=1 << 26)) == WORKSPACE
 
 
 def test_scan_workspace():
@@ -343,6 +355,50 @@ def test_norm_binding():
                       (dict(), ValueError)):
         with pytest.raises(error):
             rmsnorm.rmsnorm_bwd(**{**b, **kw})
+
+
+WRAPPED = """
+import ctypes
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from aware_conv_amd import _acts, sscan
+
+views = sscan._Views6()
+
+def f(x):
+    try:
+        _acts._lists.read(ctypes.addressof(views), x, ((("x",), (x,)),), %(flats)s)
+    except RuntimeError as e:
+        print("raised", str(e).splitlines()[0], flush=True)
+        raise KeyError("seen")
+
+with FakeTensorMode():
+    x = torch.empty(4, 3, 8, device="cuda")
+    try:
+        torch.vmap(f)(x)
+    except KeyError:
+        pass
+"""
+
+
+def test_wrapped_tensors_raise():
+    """Tensors without memory of their own, as torch's transforms make them, are refused by an
+    exception: in a process of its own, with fake tensors for those on a GPU."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for flats in ("()", '(("x", x, torch.float32, (3, 8), False),)'):
+        r = subprocess.run([sys.executable, "-c", WRAPPED % {"flats": flats}], capture_output=True, text=True, timeout=120,
+                           cwd=root)
+        assert r.returncode == 0 and r.stdout.startswith("raised"), r.stderr[-2000:]
+
+
+def test_read_refuses_what_it_cannot_take():
+    read, at = _acts._lists.read, ctypes.addressof(sscan._Views6())
+    x = torch.zeros(2, 3)
+    assert read(at, x, ((("x",), (x,)),), ()) is None  # not on a GPU
+    assert read(at, 3, (), ()) is None
+    for bad in ((at, x, [], ()), (at, x, (), None), ("a", x, (), ()), (at,)):
+        with pytest.raises(TypeError):
+            read(*bad)
 
 
 # the reference -----------------------------------------------------------------------
