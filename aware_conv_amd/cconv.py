@@ -64,7 +64,7 @@ def cconv_fwd(x, w, bias=None, h0=None, lengths=None, silu=True, y=None, *, stre
          ("lengths", lengths, i32, (B,), True)))
     dev, given = x.device, y
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _acts.like(x)
         v[1] = _view(y)
     last = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
     _lib._enqueue(dev, "cconv_fwd", _form(*shape), p, pw, pb, ph0, plen, p + VIEW,
@@ -94,7 +94,7 @@ def cconv_bwd(x, w, dy, bias=None, h0=None, dlast=None, lengths=None, silu=True,
          ("grads[dh0]", get("dh0"), x.dtype, kept, True)))
     dev = x.device
     if get("dx") is None:
-        grads["dx"] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        grads["dx"] = _acts.like(x)
         v[2] = _view(grads["dx"])
     out = []
     for n, at, size, dtype, there in (("dw", pdw, (C, K), f32, True), ("dbias", pdb, (C,), f32, bias is not None),
@@ -126,7 +126,7 @@ def cconv_step(x, w, cache, bias=None, slots=None, silu=True, y=None, *, stream=
          ("cache", cache, x.dtype, (S, K - 1, C), False), ("slots", slots, i32, (B,), True)))
     dev, given = x.device, y
     if y is None:
-        y = torch.empty((B, C), dtype=x.dtype, device=dev)
+        y = _acts.like(x)
         v[1] = _view(y)
     _lib._enqueue(dev, "cconv_step", _form(*shape), S, p, pw, pb, pcache, pslots, p + VIEW,
                   _raw_stream(stream, dev))

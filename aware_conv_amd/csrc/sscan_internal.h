@@ -24,7 +24,7 @@ struct Args {
     // where a sequence is cut into S segments of `seg` positions: what each does to a state
     float *seg_state, *seg_sum;  // [S][B][D][N] from zero; [S][B][D] sums of delta
     // partial sums of the backward pass
-    float* part_bc;  // [tiles of a group][B][T][G][2][N]
+    float* part_bc;  // [tiles of a group][B][T][G][2][waves * 4 * per_lane]
     float *part_a, *part_d, *part_bias;  // [B * S][D][N], [B * S][D] twice
     int B, T, D, N, G;
     int Dg, tiles;  // channels of a group, and workgroups for them

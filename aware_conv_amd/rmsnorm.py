@@ -81,10 +81,10 @@ def _forward(x, w, residual, eps, y, total, scale, save_rstd, stream, e4m3):
             raise ValueError("y must be like x, with adjacent elements along its rows, on %s" % dev)
         _put(v, 1, y)
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn if e4m3 else x.dtype, device=dev)
+        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev) if e4m3 else _acts.like(x)
         v[1] = y.data_ptr(), T * C, C
     if residual is not None and total is None:
-        total = torch.empty(x.shape, dtype=residual.dtype, device=dev)
+        total = _acts.like(residual)
         v[3] = total.data_ptr(), T * C, C
     if e4m3 and scale is None:
         scale = torch.empty(rows, dtype=f32, device=dev)
@@ -137,10 +137,10 @@ def rmsnorm_bwd(kept, w, rstd, dy, dtotal=None, grads=None, workspace=None, *, s
          ("grads[dw]", get("dw"), f32, (C,), True)))
     dev = dy.device
     if get("dx") is None:
-        grads["dx"] = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+        grads["dx"] = _acts.like(dy)
         _put(v, 1, grads["dx"])
     if two and get("dresidual") is None:
-        grads["dresidual"] = torch.empty(dy.shape, dtype=kept.dtype, device=dev)
+        grads["dresidual"] = _acts.like(kept)
         _put(v, 4, grads["dresidual"])
     if pdw is None:
         grads["dw"] = torch.empty(C, dtype=f32, device=dev)

@@ -79,7 +79,7 @@ def sscan_fwd(x, dt, a_log, b, c, d=None, z=None, dt_bias=None, h0=None, lengths
          ("h0", h0, f32, (B, D, N), True), ("lengths", lengths, i32, (B,), True)))
     dev, given = x.device, y
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _acts.like(x)
         v[3] = _view(y)
     h_last = torch.empty((B, D, N), dtype=f32, device=dev)
     n_states, need, _ = _sizes(*shape)
@@ -123,7 +123,7 @@ def sscan_bwd(x, dt, a_log, b, c, states, dy, d=None, z=None, dt_bias=None, dh_l
     dev = x.device
     for k, n, like in ((4, "dx", x), (5, "ddt", x), (6, "dz", z), (9, "db", b), (10, "dc", b)):
         if get(n) is None and like is not None:
-            grads[n] = torch.empty(like.shape, dtype=x.dtype, device=dev)
+            grads[n] = _acts.like(like)
             v[k] = _view(grads[n])
     out = []
     for n, at, size, there in (("da_log", pda, (D, N), True), ("dd", pdd, (D,), d is not None),
@@ -159,7 +159,7 @@ def sscan_step(x, dt, a_log, b, c, state, d=None, z=None, dt_bias=None, slots=No
          ("state", state, f32, (S, D, N), False), ("slots", slots, i32, (B,), True)))
     dev, given = x.device, y
     if y is None:
-        y = torch.empty((B, D), dtype=x.dtype, device=dev)
+        y = _acts.like(x)
         v[3] = _view(y)
     _lib._enqueue(dev, "sscan_step", _form(*shape), S, p, p + VIEW, pa, p + 4 * VIEW,
                   p + 5 * VIEW, pd, None if z is None else p + 2 * VIEW, pbias, pstate, pslots, p + 3 * VIEW,

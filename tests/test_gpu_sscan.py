@@ -372,9 +372,9 @@ def test_positions_one_by_one(N):
     assert (cache - last).abs().max() <= 1e-5 * last.abs().max()
 
 
-@pytest.mark.parametrize("B,D,N", [(40, 2100, 16), (9, 33000, 5)])
+@pytest.mark.parametrize("B,D,N", [(40, 2100, 16), (9, 33000, 5), (33, 33000, 5), (35, 33000, 16)])
 def test_many_single_positions(B, D, N):
-    """So many that a thread takes several sequences; the last group of them is not whole."""
+    """Up to so many that a thread takes two sequences (from 16384 workgroups on); the last pair is not whole."""
     import aware_conv_amd as A
     s = make(B, 1, D, N, dtype="bf16", seed=D)
     S = B + 2
