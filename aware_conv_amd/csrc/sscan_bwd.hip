@@ -4,6 +4,13 @@
 // chunk of positions to the first.  In a chunk it forms the states again from the
 // saved one, keeps those of 16 positions (8 where a lane has 4 states) in
 // registers, and runs the gradient back over them.
+//
+// The vector ALU bounds it, at two wavefronts on a SIMD, which is what the registers of
+// those states leave: 67 cycles for 64 states at four, measured for each instruction.
+// 16 states, 8 sequences of 4096 positions of 2048 channels, bf16: 1.09 ms, and 26 us
+// for the sums of db and dc over workgroups; 21 states in 3 groups, 24 x 1000 x 999,
+// fp16, ragged: 515 and 25 us.  Three wavefronts, with registers in memory: 890 for
+// 520 then; states of 8 positions at a time: 1189 for 1084; 4 states to a lane: 1198.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

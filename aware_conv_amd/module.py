@@ -163,7 +163,8 @@ class SelectiveMixer(torch.nn.Module):
         return self.outer(v), x if total is None else total, last, h
 
     def forward(self, x, residual=None, lengths=None):
-        """(output, residual stream) of x [B, T, C]; lengths [B] int32 where sequences are padded."""
+        """(output, residual stream) of x [B, T, C]; lengths [B] int32 where sequences are padded
+        (with finite values where gradients are wanted: the projections see them)."""
         return self._mix(x, residual, lengths)[:2]
 
     def new_cache(self, rows):

@@ -1,7 +1,7 @@
 /*
  * sscan.h -- C ABI of a selective state space scan over token sequences for
  * AMD Instinct MI355X (gfx950): a recurrence whose step, input and output maps
- * depend on the token, with N states per channel (Gu and Dao, "Mamba",
+ * depend on the token, with N states per channel (Gu and Dao,
  * arXiv 2312.00752, section 3).
  *
  * Per sequence, channel d of group k = d / (D / G) and state n, at position t:
