@@ -109,7 +109,11 @@ class SelectiveMixer(torch.nn.Module):
     position at a time.
 
     Norm weight, convolution and the scan's parameters are fp32 whatever the layer's dtype; the
-    steps start spread over ``step_range``, the decay rates at 1..states."""
+    steps start spread over ``step_range``, the decay rates at 1..states.
+
+    A pass with its backward can be captured into a graph, as torch's own operations can: after a
+    warm-up on another stream, and while no eager result of the same parameters that still holds
+    its graph is alive (torch would draw that one's stream into the capture, and fail)."""
 
     _FP32 = ("norm", "conv_w", "conv_b", "dt_bias", "a_log", "d")
 
