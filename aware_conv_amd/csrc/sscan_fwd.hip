@@ -237,7 +237,7 @@ hipError_t run_fwd(const Args& a, hipStream_t st) {
 template <class D, int V, int Q>
 __global__ __launch_bounds__(256) void k_step(StepArgs a) {
     using S = typename D::S;
-    const int per = (a.D + 63) / 64, seq0 = blockIdx.x / per * Q;
+    const int per = (a.D + 63) / 64, seq0 = a.first + blockIdx.x / per * Q;
     const int d = blockIdx.x % per * 64 + threadIdx.x / 4, lane = threadIdx.x & 3, group = d / a.Dg;
     if (d >= a.D) return;  // whole groups of four
     float x[Q], delta[Q], sum[Q];
@@ -312,14 +312,24 @@ __global__ __launch_bounds__(256) void k_step(StepArgs a) {
 }
 
 template <class D, int V>
-hipError_t run_step(const StepArgs& a, hipStream_t st) {
+hipError_t run_step(StepArgs a, hipStream_t st) {
     const long long per = (a.D + 63) / 64;
     // Two sequences to a thread from 16384 workgroups of one on: 4096 channels of 16 states, bf16,
     // 512 sequences 74 us by two, 83 by one, 84 by four; 256: 34 by two, 37 by one; 128 (8192
     // workgroups) 21 either way; 8: 4.2 by two, 3.8 by one.
-    if (a.B * per >= 16384) k_step<D, V, 2><<<unsigned((a.B + 1) / 2 * per), 256, 0, st>>>(a);
-    else k_step<D, V, 1><<<unsigned(a.B * per), 256, 0, st>>>(a);
-    return hipGetLastError();
+    if (a.B * per < 16384) {
+        k_step<D, V, 1><<<unsigned(a.B * per), 256, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    // a launch has fewer than 2^32 threads
+    const long long pairs = (a.B + 1LL) / 2, most = (1LL << 23) / per;
+    for (long long first = 0; first < pairs; first += most) {
+        a.first = int(2 * first);
+        k_step<D, V, 2><<<unsigned(std::min(most, pairs - first) * per), 256, 0, st>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 template <class D>
 hipError_t run_step(const StepArgs& a, hipStream_t st) {

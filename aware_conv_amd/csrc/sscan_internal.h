@@ -55,6 +55,7 @@ struct StepArgs {
     float* state;
     const int* slots;
     int B, D, N, G, Dg, S;
+    int first;  // sequence of the launch
 };
 hipError_t step(int dtype, const StepArgs& a, hipStream_t st);
 

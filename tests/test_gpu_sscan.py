@@ -471,3 +471,24 @@ def test_gradients_against_differences():
         up, down = (loss({**at, k: at[k] + sign * 2 ** -7 * way}) for sign in (1, -1))
         slope = float((p[k].grad.double() * way.double()).sum())
         assert abs((up - down) * 2 ** 6 - slope) <= 1e-3 * size, k
+
+
+@pytest.mark.parametrize("B", [1 << 25, (1 << 25) - 3])
+def test_most_single_positions(B):
+    """More sequences than one launch has threads for; one channel of one state, fp32.  Tolerance: h
+    takes four roundings, a power to 2 units and softplus to 4 of its last place; y two more."""
+    import aware_conv_amd as A
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, dt, b, c, cache = r(B, 1), r(B, 1), r(B, 1), r(B, 1), r(B, 1, 1)
+    a_log = torch.zeros(1, 1, device="cuda")
+    before = cache.clone()
+    y = A.sscan_step(x, dt, a_log, b, c, cache)
+    for part in (slice(0, 1 << 16), slice((1 << 24) - 1000, (1 << 24) + 1000), slice(B - (1 << 16), B)):
+        x_, dt_, b_, c_, h_ = (t[part].reshape(-1).double() for t in (x, dt, b, c, before))
+        delta = torch.nn.functional.softplus(dt_)
+        u = torch.exp(-delta) * h_
+        h = u + delta * x_ * b_
+        mass = u.abs() * (1 + delta) + (delta * x_ * b_).abs()
+        assert ((cache[part].reshape(-1).double() - h).abs() <= 12 * 2.0 ** -23 * mass + 1e-30).all()
+        assert ((y[part].reshape(-1).double() - c_ * h).abs() <= 14 * 2.0 ** -23 * (c_.abs() * mass) + 1e-30).all()
