@@ -19,6 +19,8 @@ int check_form(const cconv_shape* s) {
     if (s->K < 1 || s->K > CCONV_MAX_TAPS) return WTCONV_ERR_SHAPE;
     if (s->dtype != GSCAN_F32 && s->dtype != GSCAN_F16 && s->dtype != GSCAN_BF16)
         return WTCONV_ERR_DTYPE;
+    // the launch that closes the sums of C * K values has fewer than 2^32 threads
+    if ((long long)s->C * s->K > (1LL << 27)) return WTCONV_ERR_SHAPE;
     return (long long)s->B * s->C > (1LL << 31) ? WTCONV_ERR_SHAPE : WTCONV_OK;
 }
 int check_shape(const cconv_shape* s) {

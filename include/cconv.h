@@ -52,9 +52,9 @@ typedef struct {
 } cconv_shape;
 
 /*
- * Sizes: B * C up to 2^31 (WTCONV_ERR_SHAPE beyond).  What one launch does not
- * hold is refused with WTCONV_ERR_UNSUPPORTED: B * ceil(C / 128) * (ceil(T / 128) + 1)
- * has to be below 2^24.
+ * Sizes: B * C up to 2^31, C * K up to 2^27 (WTCONV_ERR_SHAPE beyond).  What one
+ * launch does not hold is refused with WTCONV_ERR_UNSUPPORTED:
+ * B * ceil(C / 128) * (ceil(T / 128) + 1) has to be below 2^24.
  */
 
 /* Bytes of device workspace that cconv_bwd needs (cconv_fwd needs none). */

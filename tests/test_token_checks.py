@@ -183,7 +183,7 @@ def cbwd(s=None, ws=far(20), nws=0, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(B=-1), SHAPE), (dict(T=-1), SHAPE), (dict(C=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=9), SHAPE),
     (dict(T=(1 << 30) + 1), SHAPE), (dict(dtype=-1), DTYPE), (dict(B=1 << 16, C=1 << 16), SHAPE),
-    (dict(B=8, T=1 << 30, C=129), UNSUPPORTED)])
+    (dict(B=1, C=(1 << 25) + 1), SHAPE), (dict(B=8, T=1 << 30, C=129), UNSUPPORTED)])
 def test_conv_shapes(call, kw, code):
     assert call(cshape(**kw)) == code
 
