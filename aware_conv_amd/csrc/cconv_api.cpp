@@ -6,6 +6,7 @@
 #include "call_buffers.h"
 #include "cconv.h"
 #include "cconv_internal.h"
+#include "close_sums.h"
 
 namespace {
 
@@ -19,7 +20,6 @@ int check_form(const cconv_shape* s) {
     if (s->K < 1 || s->K > CCONV_MAX_TAPS) return WTCONV_ERR_SHAPE;
     if (s->dtype != GSCAN_F32 && s->dtype != GSCAN_F16 && s->dtype != GSCAN_BF16)
         return WTCONV_ERR_DTYPE;
-    // the launch that closes the sums of C * K values has fewer than 2^32 threads
     if ((long long)s->C * s->K > (1LL << 27)) return WTCONV_ERR_SHAPE;
     return (long long)s->B * s->C > (1LL << 31) ? WTCONV_ERR_SHAPE : WTCONV_OK;
 }
@@ -85,6 +85,7 @@ int cconv_bwd(const cconv_shape* s, const gscan_view* x, const float* w, const f
     int rc = check_shape(s);
     if (rc) return rc;
     if (!bias != !dbias) return WTCONV_ERR_NULL;  // a term's gradient comes with the term
+    if (!calls::close_fits((long long)s->C * s->K, bias ? s->C : 0)) return WTCONV_ERR_UNSUPPORTED;
     const ccv::Plan p = ccv::plan(*s);
     const size_t e = elem_size(s->dtype);
     const long long kept = (long long)s->B * (s->K - 1) * s->C;

@@ -18,6 +18,15 @@ struct Sums {
     float* out;
 };
 
+inline long long close_blocks(long long na, long long nb, long long nc) {
+    return (na + 15) / 16 + (nb + 15) / 16 + (nc + 15) / 16;
+}
+// Whether one launch, which has fewer than 2^32 threads, closes the sums of so many
+// values; asked before anything is enqueued.
+inline bool close_fits(long long na, long long nb = 0, long long nc = 0) {
+    return close_blocks(na, nb, nc) < (1LL << 24);
+}
+
 // `tag` tells the copies of one source file from another's.
 template <int tag>
 __global__ __launch_bounds__(256) void k_close(Sums a, Sums b, Sums c, long long P) {
@@ -49,7 +58,7 @@ inline hipError_t close_sums(long long P, hipStream_t st, Sums a, Sums b = {}, S
     if (!a.out) a.n = 0;
     if (!b.out) b.n = 0;
     if (!c.out) c.n = 0;
-    const long long blocks = (a.n + 15) / 16 + (b.n + 15) / 16 + (c.n + 15) / 16;
+    const long long blocks = close_blocks(a.n, b.n, c.n);
     if (blocks == 0) return hipSuccess;
     k_close<tag><<<unsigned(blocks), 256, 0, st>>>(a, b, c, P);
     return hipGetLastError();

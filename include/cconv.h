@@ -54,7 +54,8 @@ typedef struct {
 /*
  * Sizes: B * C up to 2^31, C * K up to 2^27 (WTCONV_ERR_SHAPE beyond).  What one
  * launch does not hold is refused with WTCONV_ERR_UNSUPPORTED:
- * B * ceil(C / 128) * (ceil(T / 128) + 1) has to be below 2^24.
+ * B * ceil(C / 128) * (ceil(T / 128) + 1) has to be below 2^24, and so has, for
+ * cconv_bwd with a bias, ceil(C * K / 16) + ceil(C / 16).
  */
 
 /* Bytes of device workspace that cconv_bwd needs (cconv_fwd needs none). */
