@@ -13,8 +13,8 @@
  *
  *   scale = max |y| / 448             codes = y (1 / scale) in e4m3, to nearest even
  *
- * (a row whose scale would be below 2^-126 has scale 0 and codes 0; a NaN has the
- * code NaN).  A code depends on the last bit of what it is formed from, so codes and
+ * (a row whose scale would be below 2^-126 has scale 0 and codes 0, a row of no
+ * elements rstd NaN and scale 0; a NaN has the code NaN).  A code depends on the last bit of what it is formed from, so codes and
  * scales are defined to that bit from rstd: each operation, (s rstd) w and the
  * others as written, is in fp32 and rounded to nearest even by itself, and a product
  * beyond 448 is taken as 448.  The inverse and the product are rounded once each, so
