@@ -111,6 +111,9 @@ class SelectiveMixer(torch.nn.Module):
     Norm weight, convolution and the scan's parameters are fp32 whatever the layer's dtype; the
     steps start spread over ``step_range``, the decay rates at 1..states.
 
+    Under autocast the projections and what follows them are in its dtype; the cache's rows keep
+    the layer's (the convolution's inputs) and fp32 (the scan's states).
+
     A pass with its backward can be captured into a graph, as torch's own operations can: after a
     warm-up on another stream, and while no eager result of the same parameters that still holds
     its graph is alive (torch would draw that one's stream into the capture, and fail)."""
@@ -161,6 +164,7 @@ class SelectiveMixer(torch.nn.Module):
         """(output, stream, the convolution's last inputs, the scan's last state)"""
         y, total = rmsnorm.rms_norm(x, self.norm, self._stream(x, residual), self.eps)
         u, z = self.inner(y).chunk(2, dim=-1)
+        conv0 = None if conv0 is None else conv0.to(u.dtype)
         u, last = cconv.causal_conv(u, self.conv_w, self.conv_b, h0=conv0, lengths=lengths)
         dt, b, c = self.low(u).split(self.split, dim=-1)
         v, h = sscan.selective_scan(u, self.dt(dt), self.a_log, b, c, self.d, z, self.dt_bias, h0, lengths)
@@ -188,7 +192,8 @@ class SelectiveMixer(torch.nn.Module):
             raise ValueError("rows must be %d different rows of the cache's %d, got %s"
                              % (x.shape[0], len(state), rows))
         at = torch.tensor(rows, dtype=torch.long, device=state.device)
-        out, total, conv[at], state[at] = self._mix(x, residual, lengths, conv[at], state[at])
+        out, total, last, state[at] = self._mix(x, residual, lengths, conv[at], state[at])
+        conv[at] = last.to(conv.dtype)
         return out, total
 
     @torch.no_grad()
@@ -196,7 +201,7 @@ class SelectiveMixer(torch.nn.Module):
         """(output, residual stream) of one position x [B, C], which moves the cache's rows on."""
         y, total, _ = rmsnorm.rmsnorm_fwd(x, self.norm, residual=self._stream(x, residual), eps=self.eps)
         u, z = self.inner(y).chunk(2, dim=-1)
-        u = cconv.cconv_step(u, self.conv_w, cache[0], bias=self.conv_b, slots=slots)
+        u = cconv.cconv_step(u.to(cache[0].dtype), self.conv_w, cache[0], bias=self.conv_b, slots=slots).to(z.dtype)
         dt, b, c = self.low(u).split(self.split, dim=-1)
         v = sscan.sscan_step(u, self.dt(dt), self.a_log, b, c, cache[1], d=self.d, z=z, dt_bias=self.dt_bias,
                              slots=slots)
