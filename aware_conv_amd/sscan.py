@@ -174,16 +174,16 @@ class SelectiveScanFunction(torch.autograd.Function):
     kernel."""
 
     @staticmethod
-    def forward(ctx, x, dt, a_log, b, c, d, z, dt_bias, h0, lengths):
+    def forward(ctx, x, dt, a_log, b, c, d, z, dt_bias, h0, lengths, grad=True):
         ctx.set_materialize_grads(False)
         x, dt, b, c, z = (_acts.rows(t) for t in (x, dt, b, c, z))
         a_log, d, dt_bias, h0 = (_acts.flat(t) for t in (a_log, d, dt_bias, h0))
-        want = any(ctx.needs_input_grad[:9])
+        # needs_input_grad says what the inputs are, also where no gradient is recorded (grad=False)
+        want = grad and any(ctx.needs_input_grad[:9])
         y, h_last, states = sscan_fwd(x, dt, a_log, b, c, d=d, z=z, dt_bias=dt_bias, h0=h0, lengths=lengths,
                                       save_states=want)
         if want:
             ctx.save_for_backward(x, dt, a_log, b, c, d, z, dt_bias, lengths, states)
-            ctx.has_h0 = h0 is not None
         return y, h_last
 
     @staticmethod
@@ -195,10 +195,10 @@ class SelectiveScanFunction(torch.autograd.Function):
         g = sscan_bwd(x, dt, a_log, b, c, states, _acts.rows(dy), d=d, z=z, dt_bias=dt_bias,
                       dh_last=_acts.flat(dh_last), lengths=lengths)
         order = ("dx", "ddt", "da_log", "db", "dc", "dd", "dz", "ddt_bias", "dh0")
-        return (*[g[n] if need else None for n, need in zip(order, ctx.needs_input_grad)], None)
+        return (*[g[n] if need else None for n, need in zip(order, ctx.needs_input_grad)], None, None)
 
 
 def selective_scan(x, dt, a_log, b, c, d=None, z=None, dt_bias=None, h0=None, lengths=None):
     """(y, h_last) of the selective state space scan, differentiable in every argument but
     ``lengths``."""
-    return SelectiveScanFunction.apply(x, dt, a_log, b, c, d, z, dt_bias, h0, lengths)
+    return SelectiveScanFunction.apply(x, dt, a_log, b, c, d, z, dt_bias, h0, lengths, torch.is_grad_enabled())
