@@ -353,11 +353,25 @@ Plan plan(const sscan_shape& s, bool backward) {
     p.fits = units < (1LL << 20) && s.B * chunks < (1LL << 31);
     // One workgroup on a compute unit takes 88 ns a position forwards and 246 backwards (16 states),
     // however many others there are up to 256; a second one on it costs 30% more for both.
-    // Segments cost a pass over all but the last more.  4096 positions of 2048 channels, bf16:
-    // 8 sequences (256 workgroups) 351 us forwards whole, 430 in 4 segments; 6 (192) 361 and 510 in 2,
-    // 377 in 5; 4 (128) 361 and 263 in 4; 1 (32) 361 and 87 in 8 or 16, 110 in 32.
+    // Segments cost a pass over all but the last more, so a sequence is cut where that leaves at
+    // least three, of two workgroups on a compute unit in all.  Microseconds whole and cut, bf16,
+    // one sequence of 4096 positions (24 and 64 states: 2048), forwards with states kept / backwards:
+    //   workgroups          96          128         170         171 to 191
+    //   segments            5           4           3           2
+    //    8 states  whole    305 / 846   305 / 852   306 / 862   310 / 863
+    //              cut      159 / 351   193 / 425   251 / 557   325 / 779
+    //   16         whole    365 / 1008  371 / 1013  426 / 1026  427 / 1032
+    //              cut      221 / 535   273 / 658   370 / 874   461 / 1199
+    //   24         whole    196 / 489   196 / 492   195 / 498   202 / 500
+    //              cut      120 / 277   145 / 331   187 / 433   225 / 596
+    //   64         whole    295 / 940   296 / 962   298 / 991   297 / 998
+    //              cut      216 / 495   261 / 615   338 / 813   398 / 1110
+    // and 32 workgroups of 16 states forwards 361 whole, 87 in 8 or 16 segments, 110 in 32.
+    // Two pay backwards only, where a wavefront has all the states (up to 8).  Three may cost a
+    // forward pass more than they give: 16 states, 1024 positions 103 cut, 96 whole.
+    const long long fill = units ? 512 / units : 0, least = backward && p.waves == 1 ? 2 : 3;
     long long S = 1;
-    if (units && units < 192) S = std::max(1LL, std::min({512 / units, chunks / 8, 64LL}));
+    if (units < 192 && fill >= least) S = std::max(1LL, std::min({fill, chunks / 8, 64LL}));
     const long long per = (chunks + S - 1) / S;
     p.seg = int(std::max(1LL, per) * kChunk);
     p.S = int(std::max(1LL, per ? (chunks + per - 1) / per : 1));
