@@ -1,13 +1,21 @@
 // Root-mean-square norm with the residual's addition (include/rmsnorm.h).
 //
-// HBM bounds it.  A row is read once and kept in the registers of a wavefront, or
-// of a workgroup where it is longer, and written from there; only rows of more
-// than 32768 elements are read again.  Elements go 8 at a time, whatever their
-// alignment, and past the caches on their way out.  32768 rows of 2048 with a
-// residual in fp32, bf16: forwards 154 us (805 MB, 5.2 TB/s), backwards 198 us
-// (4.1 TB/s) and 10 us for the weight's sums; 16384 rows of 4096 with a residual,
-// bf16, output in 8 bits: 95 us (470 MB, 5.0 TB/s); 23976 rows of 999, fp16, no two
-// rows aligned alike: 40, 59 and 8 us (4.8 and 4.1 TB/s).
+// HBM bounds it for rows of 256 elements and more.  A row is read once and kept in
+// the registers of a wavefront, or of a workgroup where it is longer, and written
+// from there; only rows of more than 32768 elements are read again.  Elements go 8
+// at a time, whatever their alignment, and past the caches on their way out.  32768
+// rows of 2048 with a residual in fp32, bf16: forwards 154 us (805 MB, 5.2 TB/s),
+// backwards 198 us (the sum, dy and dtotal in, dx and the residual's gradient out,
+// 1074 MB, 5.4 TB/s) and 10 us for the weight's sums; 16384 rows of 4096 with a
+// residual, bf16, output in 8 bits: 95 us (470 MB, 5.0 TB/s); 23976 rows of 999,
+// fp16, no two rows aligned alike: 40, 58 and 8 us (192 MB each way: 4.8 and 3.3 TB/s;
+// backwards dtotal is asked for only after the row's sum is known).
+//
+// Narrow rows leave lanes idle, 8 elements to a lane and a wavefront to a row: 64M
+// elements, bf16 with a residual, rows of 256, 128, 64, 16: forwards 111, 197, 387,
+// 1589 us, backwards 170, 296, 546, 2032 (rows of 1024: 77 and 109).  Rows of 16385
+// to 32768 elements have 32 a lane in 16 wavefronts, whose 128 registers do not hold
+// them backwards (110 are spilled): 32768 forwards 96 us, backwards 278.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -5,12 +5,18 @@
 // saved one, keeps those of 16 positions (8 where a lane has 4 states) in
 // registers, and runs the gradient back over them.
 //
-// The vector ALU bounds it, at two wavefronts on a SIMD, which is what the registers of
-// those states leave: 67 cycles for 64 states at four, measured for each instruction.
-// 16 states, 8 sequences of 4096 positions of 2048 channels, bf16: 1.09 ms, and 26 us
-// for the sums of db and dc over workgroups; 21 states in 3 groups, 24 x 1000 x 999,
-// fp16, ragged: 515 and 25 us.  Three wavefronts, with registers in memory: 890 for
-// 520 then; states of 8 positions at a time: 1189 for 1084; 4 states to a lane: 1198.
+// The vector ALU bounds it, at two wavefronts on a SIMD: 499 plain instructions, 248
+// with a DPP modifier, 42 transcendental and 36 lane exchanges for a chunk of 128
+// states to a wavefront, 3290 cycles by what each takes (sscan_math.h).
+// 16 states, 8 sequences of 4096 positions of 2048 channels, bf16: 1.02 ms, of which
+// that is 0.70, and 26 us for the sums of db and dc over workgroups; one workgroup of
+// eight wavefronts to a compute unit is all there is in this case.  21 states in 3
+// groups, 24 x 1000 x 999, fp16, ragged: 515 and 25 us; its workgroups of six
+// wavefronts take 202 registers a lane, of which two do not fit a compute unit.  Three
+// wavefronts, with registers in memory: 890 for 520 there; states of 8 positions at a
+// time: 1189 for 1084 in the other case; 4 states to a lane: 1198.  With 33 to 64
+// states, 4 to a lane, 16 to 77 registers are spilled: 48 states 6.3 ms, 64 4.0 ms for
+// the 2.0 of 32.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

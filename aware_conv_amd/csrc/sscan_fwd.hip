@@ -13,11 +13,14 @@ constexpr int kPad = 18;  // float2s between two channels' rows in LDS: no bank 
 // SUMS: the pass that gives y.  Otherwise: what a segment does to a state that
 // starts from zero, and its sum of delta (with which the state it starts from decays).
 //
-// The vector ALU bounds it (22 cycles of a SIMD for 64 states, sscan_math.h), with two
-// wavefronts on a SIMD half as much again.  16 states, bf16: 8 sequences of 4096
-// positions of 2048 channels 450 us (350 where no states are saved), of which HBM
-// would take 110; one of 65521 of 2560 channels, whose 40 workgroups become 480 by
-// cutting it into segments, 530 us for what the segments do and 860 for y.
+// The vector ALU bounds it: of a tile's turn 167 plain instructions, 64 with a DPP
+// modifier, 40 transcendental and 12 lane exchanges, 1140 cycles of a SIMD by what
+// each takes at four wavefronts and 1240 at two (694 of them are the states' own steps,
+// sscan_math.h); 720 in the pass over segments.  16 states, bf16: 8 sequences of 4096
+// positions of 2048 channels 435 us (362 where no states are saved), of which two
+// wavefronts' instructions are 264 and HBM would take 110; one of 65521 of 2560
+// channels, whose 40 workgroups become 480 by cutting it into segments, 520 us for
+// what the segments do (350 by instructions) and 840 for y (610).
 //
 // In a tile's turn the wavefronts compute from the delta and u in one half of LDS,
 // then put those of the next tile into the other half, and, past the barrier,
@@ -344,6 +347,9 @@ Plan plan(const sscan_shape& s, bool backward) {
     // Two states to a lane wherever there are that many, divided among up to four wavefronts.
     // 16 states, 8 sequences of 4096 positions of 2048 channels, forwards and backwards: two to a
     // lane 450 and 1090 us; one to a lane, in four wavefronts, 450 and 1200; four, in one, 3660 backwards.
+    // Measured at 16 states alone.  As divided here, other numbers of states, the same otherwise:
+    // 4: 274 and 681; 8 (one wavefront): 325 and 853; 24: 677 and 1949; 32: 618 and 2002; 48: 1405 and
+    // 6332; 64: 1279 and 3980.
     p.per_lane = q <= 1 ? 1 : q <= 8 ? 2 : 4;
     p.waves = (q + p.per_lane - 1) / p.per_lane;
     p.width = p.waves <= 2 ? 64 : 32;

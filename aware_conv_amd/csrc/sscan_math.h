@@ -9,9 +9,9 @@
 // position i's value to the whole row.  So the innermost step of a state,
 // h = exp2(delta A') h + u b, s += c h, is five instructions, and reads nothing from
 // memory but the position's delta and u, which LDS holds.  On this chip it takes
-// 2.4 + 8.3 + 4.3 + 2.4 + 4.3 cycles of a SIMD where four wavefronts share it, half
-// as much again with two, and twice that with one: states are therefore
-// divided among NB wavefronts of the same channels.
+// 2.4 + 8.3 + 4.3 + 2.4 + 4.3 = 22 cycles of a SIMD where four wavefronts share it, 27
+// with two and 42 with one: states are therefore divided among NB wavefronts of the
+// same channels.
 //
 // A workgroup has CT x NB wavefronts.  The elements of a tile, 16 positions of its
 // 16 CT channels, are divided among all of them, channels along the lanes, so that
